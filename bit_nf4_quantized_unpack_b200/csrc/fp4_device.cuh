@@ -1,0 +1,106 @@
+// fp4_device.cuh -- storage of microscaled 4-bit floating-point matrices (MXFP4, NVFP4):
+// block sizes, the tiled scale layout, and the conversions of codes and scales.
+#pragma once
+
+#include <cstdint>
+
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace qlora {
+
+enum class Fp4 { kMx = QLORA_FP4_MX, kNv = QLORA_FP4_NV };
+
+// Values per block scale.
+template <Fp4 F>
+constexpr int kFp4Block = F == Fp4::kMx ? 32 : 16;
+// Columns that one 512-byte scale tile (128 rows x 4 blocks) covers.
+template <Fp4 F>
+constexpr int kFp4TileCols = 4 * kFp4Block<F>;
+
+// Largest magnitude of an NVFP4 value in units of gscale: E2M1 6 times E4M3 448.
+constexpr float kNvTop = 2688.f;
+
+// Byte of (row, block) in the tiled scale array, ktiles = scale tiles along a row. The
+// 512-byte tile is the order in which tcgen05.cp.32x128b.warpx4 spreads 128 rows over the
+// 32 lanes x 4 columns of tensor memory that a block-scaled MMA reads.
+__host__ __device__ __forceinline__ int64_t fp4_scale_offset(int64_t row, int64_t block,
+                                                             int64_t ktiles) {
+  return ((row >> 7) * ktiles + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+         (block & 3);
+}
+
+// Eight fp32 values -> eight E2M1 codes (nearest, ties to the even code, 6 at most), value i
+// in bits 4i..4i+3.
+__device__ __forceinline__ uint32_t fp4_pack8(const float (&v)[8]) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(d)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return d;
+}
+
+// Eight E2M1 codes -> four pairs of fp16 values (exact), pair i holding codes 2i, 2i + 1.
+__device__ __forceinline__ void fp4_unpack8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// fp32 -> E4M3 bits (nearest, ties to even, 448 at most).
+__device__ __forceinline__ uint32_t e4m3_bits(float x) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.f), "f"(x));
+  return d & 0xFFu;
+}
+
+// Value of a scale byte.
+template <Fp4 F>
+__device__ __forceinline__ float fp4_scale_value(uint32_t b) {
+  if (F == Fp4::kMx)  // 2^(b - 127); 2^-127 is a subnormal, 255 is NaN
+    return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+
+// Scale byte of a block that holds a NaN or an infinity.
+template <Fp4 F>
+constexpr uint32_t kFp4NanScale = F == Fp4::kMx ? 0xFFu : 0x7Fu;
+
+// Exponent e of the NVFP4 gscale 2^e of a set of values whose largest magnitude is `top`
+// (fp32 bits): the smallest e >= -126 with top <= 2688 * 2^e; 0 for top = 0.
+// 2688 = 1.3125 * 2^11, and 1.3125 has the mantissa field 0x280000.
+__device__ __forceinline__ int nv_gscale_exp(uint32_t top) {
+  if (top == 0u) return 0;
+  const int e = static_cast<int>(top >> 23) - 127 - 11 + ((top & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+  return max(e, -126);  // subnormal tops have the exponent field 0 and end here too
+}
+// 2^e for -127 <= e <= 127.
+__device__ __forceinline__ float pow2_f32(int e) {
+  return __uint_as_float(e == -127 ? 0x00400000u : static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Magnitude bits of x, 0 and `bad` set for NaN and infinities (they never enter a maximum).
+__device__ __forceinline__ uint32_t finite_mag(float x, bool& bad) {
+  const uint32_t m = __float_as_uint(x) & 0x7FFFFFFFu;
+  if (m >= 0x7F800000u) {
+    bad = true;
+    return 0u;
+  }
+  return m;
+}
+
+}  // namespace qlora

@@ -735,10 +735,13 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
 //   plain fp32 [M, r]; bf16 hi/lo of scale * v [M, 128] (the K-extension operand);
 //   bf16 hi/lo of v [M, 128] (operand of the LoRA gradients).
 //   With t_in, also the bf16 hi/lo pair [M, 128] of that fp32 [M, r] (into t_hilo).
+//   With ga (one per row) and gb (one), scale * v is divided by both first: the operand of
+//   a product whose accumulator is multiplied by them at the end.
 __global__ void k_finalize_rank(const float* __restrict__ part, int splits, int64_t rows_pad,
                                 int64_t M, int r, float scale, float* __restrict__ plain,
                                 uint16_t* __restrict__ scaled, uint16_t* __restrict__ hilo,
-                                const float* __restrict__ t_in, uint16_t* __restrict__ t_hilo) {
+                                const float* __restrict__ t_in, uint16_t* __restrict__ t_hilo,
+                                const float* __restrict__ ga, const float* __restrict__ gb) {
   griddep_wait_and_release();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= M * 64) return;
@@ -760,7 +763,9 @@ __global__ void k_finalize_rank(const float* __restrict__ part, int splits, int6
   if (j >= r) v = 0.f;
   if (plain && j < r) plain[m * r + j] = v;
   if (scaled) {  // [M, 128]: bf16 hi | bf16 lo of scale * v
-    const float sv = v * scale;
+    float sv = v * scale;
+    if (ga) sv /= ga[m];
+    if (gb) sv /= *gb;
     const uint16_t hi = bf16_bits_rn(sv);
     scaled[m * 128 + j] = hi;
     scaled[m * 128 + 64 + j] = bf16_bits_rn(sv - __uint_as_float(static_cast<uint32_t>(hi) << 16));
@@ -867,26 +872,6 @@ size_t partial_floats(int64_t rows, int64_t contraction, int nc) {
   return static_cast<size_t>(p.splits) * p.rows_pad * 64;
 }
 
-// Launch on `st` with programmatic stream serialization: the kernel may begin (its
-// prologue) while the stream's previous kernel drains; every kernel of this file waits
-// for its predecessor with griddep_wait_and_release before it touches global memory.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t st, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  note_launches(1);
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
-
 // G and T of a column-sharded backward (plain fp32 [M, r]; G summed over the shards) as
 // the bf16 operand pairs of the fused dX kernel and the grouped dA/dB GEMM: scale G as
 // hi | lo ([M, 128]), G as hi | lo and T as hi | lo (the arithmetic of k_finalize_rank).
@@ -972,20 +957,6 @@ cudaError_t run_fused(const CUtensorMap& ta, const CUtensorMap& tw, const CUtens
 
 inline unsigned blocks_for(int64_t n, int t) { return static_cast<unsigned>((n + t - 1) / t); }
 
-// Workspace carving: a bump allocator over the caller's buffer.
-struct Carve {
-  char* base;
-  size_t off = 0;
-  explicit Carve(void* b) : base(static_cast<char*>(b)) {}
-  template <typename T>
-  T* take(size_t count) {
-    off = align_up(off, 256);
-    T* p = reinterpret_cast<T*>(base ? base + off : nullptr);
-    off += count * sizeof(T);
-    return p;
-  }
-};
-
 size_t fwd_layout(const LinearShape& s, void* ws, float** part, uint16_t** ts) {
   Carve c(ws);
   *part = c.take<float>(partial_floats(s.M, s.K, 64));
@@ -1007,19 +978,10 @@ size_t bwd_layout(const LinearShape& s, void* ws, float** part, uint16_t** gs, u
   return c.off + 256;
 }
 
-#define QL_TRY(expr)                                  \
-  do {                                                \
-    cudaError_t _e = (expr);                          \
-    if (_e != cudaSuccess) return cuda_status(_e);    \
-  } while (0)
-#define QL_MAP(...)                                                    \
-  do {                                                                 \
-    if (!make_tmap_2d(__VA_ARGS__)) return QLORA_ERR_CUDA;             \
-  } while (0)
-
 // T = X A (fp32, split partials) then T_save / bf16(scale T).
 qlora_status lora_down_T(const uint16_t* X, const uint16_t* A, const LinearShape& s, float* part,
-                         float* t_plain, uint16_t* t_scaled, cudaStream_t st) {
+                         float* t_plain, uint16_t* t_scaled, cudaStream_t st,
+                         const float* ga = nullptr, const float* gb = nullptr) {
   CUtensorMap ta, tb;
   QL_MAP(&ta, kBF16, X, s.K, s.M, s.K * 2, 64, 128, kSW128);   // X K-major
   QL_MAP(&tb, kBF16, A, s.r, s.K, s.r * 2, 64, 64, kSW128);    // A as MN-major (j inner)
@@ -1028,7 +990,7 @@ qlora_status lora_down_T(const uint16_t* X, const uint16_t* A, const LinearShape
   const int64_t rows_pad = plan_split(s.M, s.K).rows_pad;
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                     splits, rows_pad, s.M, s.r, s.scale, t_plain, t_scaled, nullptr, nullptr,
-                    nullptr));
+                    nullptr, ga, gb));
   return QLORA_OK;
 }
 
@@ -1138,7 +1100,7 @@ qlora_status gemm_backward(const uint16_t* dY, const uint16_t* X, const float* T
     QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
     QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                       splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, gs, ghl,
-                      t, thl));
+                      t, thl, nullptr, nullptr));
   }
 
   // dX = dY W_hat + scale G A^T, and the grouped dA = scale X^T G (rows k) with
@@ -1218,7 +1180,7 @@ qlora_status gemm_shard_g(const uint16_t* dY, const uint16_t* B, const LinearSha
   QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                     splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, G_part, nullptr,
-                    nullptr, nullptr, nullptr));
+                    nullptr, nullptr, nullptr, nullptr, nullptr));
   return QLORA_OK;
 }
 
@@ -1297,6 +1259,127 @@ qlora_status gemm_shard_bwd(const uint16_t* dY, const uint16_t* X, const float* 
     if (ej == cudaSuccess) ej = cudaStreamWaitEvent(st, side->join, 0);
     if (e == cudaSuccess) e = ej;
   }
+  QL_TRY(e);
+  return QLORA_OK;
+}
+
+// ---- the linear layer on a microscaled 4-bit weight: the same rank-r products, with the
+// 16-bit X and dY; only the large product sees their 4-bit form.
+namespace {
+qlora_fp4_matrix carve_fp4(Carve& c, int64_t rows, int64_t cols, int format, Fp4Out* out) {
+  out->codes = c.take<uint8_t>(static_cast<size_t>(rows) * (cols / 2));
+  out->scales = c.take<uint8_t>(fp4_scales_bytes(rows, cols, format));
+  out->gscale = format == QLORA_FP4_NV ? c.take<float>(rows) : nullptr;
+  return qlora_fp4_matrix{out->codes, out->scales, out->gscale, rows, rows, cols, format};
+}
+
+size_t fp4_fwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matrix* x, Fp4Out* xo,
+                      float** part, uint16_t** ts) {
+  Carve c(ws);
+  *x = carve_fp4(c, s.M, s.K, format, xo);
+  *part = c.take<float>(partial_floats(s.M, s.K, 64));
+  *ts = c.take<uint16_t>(static_cast<size_t>(s.M) * 128);
+  return c.off + 256;
+}
+
+size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matrix* y, Fp4Out* yo,
+                      void** rest) {
+  Carve c(ws);
+  *y = carve_fp4(c, s.M, s.N, format, yo);
+  *rest = c.take<char>(0);
+  return c.off;
+}
+}  // namespace
+
+size_t fp4_fwd_workspace(const LinearShape& s, int format) {
+  qlora_fp4_matrix x;
+  Fp4Out o;
+  float* p;
+  uint16_t* t;
+  return fp4_fwd_layout(s, format, nullptr, &x, &o, &p, &t);
+}
+
+size_t fp4_bwd_workspace(const LinearShape& s, int format) {
+  qlora_fp4_matrix y;
+  Fp4Out o;
+  void* rest;
+  return fp4_bwd_layout(s, format, nullptr, &y, &o, &rest) + gemm_bwd_workspace(s);
+}
+
+qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uint16_t* A,
+                         const uint16_t* B, const LinearShape& s, uint16_t* Y, float* T_save,
+                         void* ws, cudaStream_t st) {
+  qlora_fp4_matrix x;
+  Fp4Out xo;
+  float* part;
+  uint16_t* ts;
+  fp4_fwd_layout(s, w.format, ws, &x, &xo, &part, &ts);
+  QL_TRY(launch_fp4_quantize(X, true, s.M, s.K, w.format, xo, st));
+  qlora_status q = lora_down_T(X, A, s, part, T_save, ts, st, x.gscale, w.gscale);
+  if (q != QLORA_OK) return q;
+  const Fp4Ext ext{B, ts, s.r, true};
+  return fp4_product(x, w, &ext, Y, false, st);
+}
+
+qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_saved,
+                          const qlora_fp4_matrix& wt, const uint16_t* A, const uint16_t* B,
+                          const LinearShape& s, uint16_t* dX, float* dA, float* dB, void* ws,
+                          cudaStream_t st) {
+  qlora_fp4_matrix y;
+  Fp4Out yo;
+  void* rest;
+  fp4_bwd_layout(s, wt.format, ws, &y, &yo, &rest);
+  float *part, *tbuf;
+  uint16_t *gs, *ghl, *thl;
+  bwd_layout(s, rest, &part, &gs, &ghl, &thl, &tbuf);
+  const float* t = T_saved;
+  if (!t) {
+    qlora_status q = lora_down_T(X, A, s, part, tbuf, nullptr, st);
+    if (q != QLORA_OK) return q;
+    t = tbuf;
+  }
+  if (dX) QL_TRY(launch_fp4_quantize(dY, true, s.M, s.N, wt.format, yo, st));
+  CUtensorMap ta, tb, ga, gb, ga1, gb1;
+  int splits = 0;
+  QL_MAP(&ta, kBF16, dY, s.N, s.M, s.N * 2, 64, 128, kSW128);  // dY K-major (over n)
+  QL_MAP(&tb, kBF16, B, s.N, s.r, s.N * 2, 64, 64, kSW128);    // B [r, N] K-major
+  QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
+  QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
+                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, gs, ghl, t,
+                    thl, dX ? y.gscale : nullptr, dX ? wt.gscale : nullptr));
+  QL_MAP(&ga, kBF16, X, s.K, s.M, s.K * 2, 64, 64, kSW128);    // X as MN-major (k inner)
+  QL_MAP(&gb, kBF16, ghl, 128, s.M, 256, 64, 64, kSW128);      // G hi/lo MN-major
+  QL_MAP(&ga1, kBF16, dY, s.N, s.M, s.N * 2, 64, 64, kSW128);  // dY as MN-major (n inner)
+  QL_MAP(&gb1, kBF16, thl, 128, s.M, 256, 64, 64, kSW128);     // T hi/lo MN-major
+  // dA and dB beside dX, as in gemm_backward
+  SideStream* side = nullptr;
+  if (dX) QL_TRY(side_stream(st, &side));
+  cudaStream_t gst = st;
+  if (side) {
+    QL_TRY(cudaEventRecord(side->fork, st));
+    QL_TRY(cudaStreamWaitEvent(side->st, side->fork, 0));
+    gst = side->st;
+  }
+  qlora_status q = QLORA_OK;
+  if (dX) {
+    const Fp4Ext ext{A, gs, s.r, false};
+    q = fp4_product(y, wt, &ext, dX, false, st);
+  }
+  cudaError_t e = cudaSuccess;
+  if (q == QLORA_OK)
+    e = run_lora_gemm<true, true, 128>(ga, gb, s.K, s.M, part, gst, &splits, &ga1, &gb1, s.N);
+  if (q == QLORA_OK && e == cudaSuccess) {
+    const int64_t stacked = stacked_rows(s.K, s.N);
+    e = launch_pdl(k_finalize_grad, dim3(blocks_for(stacked, kGradRows)), dim3(256), 0, gst, part,
+                   splits, plan_split(stacked, s.M).rows_pad,
+                   static_cast<int64_t>(align_up(s.K, 128)), s.K, dA, s.N, dB, s.r, s.scale);
+  }
+  if (side) {  // the caller's stream continues once both branches are done (on every path)
+    cudaError_t ej = cudaEventRecord(side->join, side->st);
+    if (ej == cudaSuccess) ej = cudaStreamWaitEvent(st, side->join, 0);
+    if (e == cudaSuccess) e = ej;
+  }
+  if (q != QLORA_OK) return q;
   QL_TRY(e);
   return QLORA_OK;
 }

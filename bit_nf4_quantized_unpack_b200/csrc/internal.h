@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -54,6 +55,53 @@ qlora_status check_linear(int64_t M, const qlora_nf4_weight& w, int r, float sca
 void profile_events(cudaEvent_t* before, cudaEvent_t* after);
 void note_launches(int n);                         // count kernels enqueued (qlora_launch_count)
 
+// ---- launch, workspace and error helpers ------------------------------------------
+// Launch on `st` with programmatic stream serialization: the kernel may begin (its
+// prologue) while the stream's previous kernel drains; every kernel launched this
+// way waits for its predecessor with griddep_wait_and_release before it touches global memory.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launches(1);
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Workspace carving: a bump allocator over the caller's buffer.
+struct Carve {
+  char* base;
+  size_t off = 0;
+  explicit Carve(void* b) : base(static_cast<char*>(b)) {}
+  template <typename T>
+  T* take(size_t count) {
+    off = align_up(off, 256);
+    T* p = reinterpret_cast<T*>(base ? base + off : nullptr);
+    off += count * sizeof(T);
+    return p;
+  }
+};
+
+#define QL_TRY(expr)                                  \
+  do {                                                \
+    cudaError_t _e = (expr);                          \
+    if (_e != cudaSuccess) return cuda_status(_e);    \
+  } while (0)
+#define QL_MAP(...)                                                    \
+  do {                                                                 \
+    if (!make_tmap_2d(__VA_ARGS__)) return QLORA_ERR_CUDA;             \
+  } while (0)
+
 // ---- launchers (codec.cu) -------------------------------------------------------
 size_t quantize_workspace_bytes(int64_t n, int64_t k);
 cudaError_t launch_quantize(const void* W, bool w_bf16, int64_t n, int64_t k, int codebook,
@@ -98,7 +146,38 @@ qlora_status decode_forward(const uint16_t* X, const qlora_nf4_weight& w, const 
                             const uint16_t* B, const LinearShape& s, uint16_t* Y,
                             float* T_save, void* ws, cudaStream_t st);
 
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+// ---- microscaled 4-bit floating point (fp4_codec.cu, fp4_gemm.cu) -----------------
+struct Fp4Out { uint8_t* codes; uint8_t* scales; float* gscale; };
+int64_t fp4_ktiles(int64_t cols, int format);  // scale tiles along a row
+inline size_t fp4_scales_bytes(int64_t rows, int64_t cols, int format) {
+  return static_cast<size_t>((rows + 127) / 128) * fp4_ktiles(cols, format) * 512;
+}
+cudaError_t launch_fp4_quantize(const void* X, bool bf16, int64_t rows, int64_t cols, int format,
+                                const Fp4Out& out, cudaStream_t st);
+cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int64_t k, int format,
+                                       const Fp4Out& w, const Fp4Out& wt, void* ws,
+                                       cudaStream_t st);
+cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st);
+// The rank-r term added to a product a b^T: sum_j p[j, n] q[m, j] with q as bf16 hi | lo
+// pairs [M, 128], in units of the two gscales; p is [r, N] (mn_major) or [N, r].
+struct Fp4Ext {
+  const uint16_t* p;
+  const uint16_t* q;
+  int r;
+  bool mn_major;
+};
+qlora_status fp4_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
+                         void* out, bool out_f32, cudaStream_t st);
+// The linear layer on a microscaled weight (gemm.cu): w is W [N, K], wt its transposed copy.
+size_t fp4_fwd_workspace(const LinearShape& s, int format);
+size_t fp4_bwd_workspace(const LinearShape& s, int format);
+qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uint16_t* A,
+                         const uint16_t* B, const LinearShape& s, uint16_t* Y, float* T_save,
+                         void* ws, cudaStream_t st);
+qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_saved,
+                          const qlora_fp4_matrix& wt, const uint16_t* A, const uint16_t* B,
+                          const LinearShape& s, uint16_t* dX, float* dA, float* dB, void* ws,
+                          cudaStream_t st);
 
 // ---- launchers (selftest.cu) ----------------------------------------------------
 cudaError_t launch_wait_selftest(cudaStream_t st);

@@ -108,6 +108,15 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* map, uin
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
+// `bytes` (a multiple of 16) from 16-byte aligned global memory into shared memory.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(smem_dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 // 2D tiled store of one box from shared memory into global memory (bulk async-group of
 // the issuing thread); elements outside the tensor are not written.
 __device__ __forceinline__ void tma_store_2d(const void* map, const void* smem_src, int x, int y) {
@@ -164,6 +173,36 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// Block-scaled E2M1 product: D[tmem] (+)= (A * SFA) (B * SFB)^T over 64 values of K. VEC = 4:
+// blocks of 16 with E4M3 scales, 2: blocks of 32 with power-of-two scales; sfa, sfb are the
+// tensor-memory addresses of the scales.
+template <int VEC>
+__device__ __forceinline__ void umma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  if constexpr (VEC == 4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// 512 bytes of shared memory (32 rows x 16 bytes) -> 4 columns of tensor memory, the same in
+// each of the four lane quarters. Ordered before the MMAs this thread issues later.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
 }
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -224,6 +263,28 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
   d |= static_cast<uint64_t>(1) << 46;  // descriptor version for sm_100
   d |= static_cast<uint64_t>(2) << 61;  // SWIZZLE_128B
   return d;
+}
+
+// Descriptor of a 512-byte scale tile for tmem_cp_scales: no swizzle, 8-row groups of 16-byte
+// rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128 >> 4) << 16;
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;  // descriptor version for sm_100
+  return d;
+}
+
+// Instruction descriptor of tcgen05.mma kind::mxf4nvf4: E2M1 A and B (K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool pow2_scales, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4)             // B scales: first byte of the column
+         | (1u << 7)                                     // A format: E2M1
+         | (1u << 10)                                    // B format: E2M1
+         | (static_cast<uint32_t>(N >> 3) << 17)         // N / 8
+         | (static_cast<uint32_t>(pow2_scales) << 23)    // scales: E8M0 or E4M3
+         | (static_cast<uint32_t>(M >> 4) << 24)         // M / 16
+         | (static_cast<uint32_t>(sf_id) << 29);         // A scales: first byte of the column
 }
 
 // Instruction descriptor of tcgen05.mma kind::f16: bf16 A and B, fp32 D.

@@ -10,6 +10,13 @@ Names follow the C entry points:
     qlora_linear_fwd(X, w, A, B, scale)               -> (Y, T)
     qlora_linear_bwd(dY, X, T, w, A, B, scale)        -> (dX, dA, dB)
     qlora_adamw_step(p, g, state, step, ...)          (in place; paged states: PagedBuffer)
+Microscaled 4-bit floating point (MXFP4, NVFP4):
+    qlora_fp4_quantize(X, fmt)                        -> FP4Matrix
+    qlora_fp4_quantize_weight(W, fmt)                 -> FP4Weight
+    qlora_fp4_dequant(q, dtype)                       -> values
+    qlora_fp4_matmul(a, b, dtype)                     -> a b^T
+    qlora_fp4_linear_fwd(X, w, A, B, scale)           -> (Y, T)
+    qlora_fp4_linear_bwd(dY, X, T, w, A, B, scale)    -> (dX, dA, dB)
 """
 from __future__ import annotations
 
@@ -37,6 +44,12 @@ class CNF4Weight(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("c2", ctypes.c_void_p), ("c1", ctypes.c_void_p),
                 ("mean", ctypes.c_void_p), ("n_out", ctypes.c_int64), ("k_in", ctypes.c_int64),
                 ("codebook", ctypes.c_int32)]
+
+
+class CFP4Matrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("gscale", ctypes.c_void_p), ("gscale_rows", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("format", ctypes.c_int32)]
 
 
 class CAdamwHparams(ctypes.Structure):
@@ -86,6 +99,19 @@ _SIGNATURES = {
     "qlora_paged_alloc": (_i32, [ctypes.POINTER(ctypes.c_void_p), _sz]),
     "qlora_paged_free": (_i32, [_vp]),
     "qlora_paged_prefetch": (_i32, [_vp, _sz, _i32, _vp]),
+    "qlora_fp4_scales_bytes": (_sz, [_i64, _i64, _i32]),
+    "qlora_fp4_quantize": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "qlora_fp4_quantize_weight_workspace_size": (_sz, []),
+    "qlora_fp4_quantize_weight": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp,
+                                         _vp, _sz, _vp]),
+    "qlora_fp4_dequant": (_i32, [CFP4Matrix, _i32, _vp, _vp]),
+    "qlora_fp4_matmul": (_i32, [CFP4Matrix, CFP4Matrix, _i32, _vp, _vp]),
+    "qlora_fp4_linear_fwd_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "qlora_fp4_linear_fwd": (_i32, [_vp, _i64, CFP4Matrix, _vp, _vp, _i32, _f32, _vp, _vp, _vp,
+                                    _sz, _vp]),
+    "qlora_fp4_linear_bwd_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "qlora_fp4_linear_bwd": (_i32, [_vp, _vp, _vp, _i64, CFP4Matrix, _vp, _vp, _i32, _f32, _vp,
+                                    _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -443,3 +469,231 @@ def qlora_adamw_step(p: torch.Tensor, g: torch.Tensor, state, step: int, *, lr: 
     hp = CAdamwHparams(lr, beta1, beta2, eps, weight_decay, step)
     _check(lib().qlora_adamw_step(_ptr(p), _ptr(p_bf16), _ptr(g), p.numel(), state_bits, sptr,
                                   sbytes, hp, _stream()), "qlora_adamw_step")
+
+
+# ------------------------------------------- microscaled 4-bit floating point (MXFP4, NVFP4)
+FP4_MXFP4, FP4_NVFP4 = 0, 1
+_FP4_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+@dataclass
+class FP4Matrix:
+    """A matrix [rows, cols] of E2M1 codes with block scales along its rows (device)."""
+    codes: torch.Tensor                 # uint8 [rows, cols / 2]
+    scales: torch.Tensor                # uint8, the tiled order of include/qlora.h
+    gscale: torch.Tensor | None         # float32 [1] or [rows]; None stands for 1
+    rows: int
+    cols: int
+    fmt: int = FP4_NVFP4
+
+    def c_struct(self) -> CFP4Matrix:
+        g = self.gscale
+        return CFP4Matrix(self.codes.data_ptr(), self.scales.data_ptr(),
+                          None if g is None else g.data_ptr(), 0 if g is None else g.numel(),
+                          self.rows, self.cols, self.fmt)
+
+    @staticmethod
+    def empty(rows: int, cols: int, fmt: int = FP4_NVFP4, device="cuda",
+              gscale_rows: int | None = None) -> "FP4Matrix":
+        """Uninitialised storage; gscale_rows: rows (default) or 1, NVFP4 only."""
+        nsc = int(lib().qlora_fp4_scales_bytes(rows, cols, fmt))
+        if rows and nsc == 0:
+            raise QLoraError(2, "FP4Matrix", f"[{rows}, {cols}], format {fmt}")
+        ng = rows if gscale_rows is None else gscale_rows
+        return FP4Matrix(torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
+                         torch.empty(nsc, dtype=torch.uint8, device=device),
+                         torch.empty(ng, dtype=torch.float32, device=device)
+                         if fmt == FP4_NVFP4 else None, rows, cols, fmt)
+
+
+@dataclass
+class FP4Weight:
+    """A weight W [n_out, k_in] and, for the gradient of the input, its transposed copy."""
+    w: FP4Matrix
+    wt: FP4Matrix | None = None
+
+
+def _fp4_tensor(t: torch.Tensor, name: str, dtypes, shape=None) -> torch.Tensor:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _fp4_matrix(q: FP4Matrix, name: str) -> FP4Matrix:
+    """Checks that the buffers hold what the sizes say, so that no kernel reads past them."""
+    _fp4_tensor(q.codes, f"{name}.codes", (torch.uint8,))
+    _fp4_tensor(q.scales, f"{name}.scales", (torch.uint8,))
+    if q.codes.numel() != q.rows * (q.cols // 2):
+        raise ValueError(f"{name}.codes: {q.codes.numel()} bytes for [{q.rows}, {q.cols}]")
+    if q.scales.numel() != int(lib().qlora_fp4_scales_bytes(q.rows, q.cols, q.fmt)):
+        raise ValueError(f"{name}.scales: {q.scales.numel()} bytes for [{q.rows}, {q.cols}]")
+    if q.gscale is not None:
+        _fp4_tensor(q.gscale, f"{name}.gscale", (torch.float32,))
+        if q.gscale.numel() not in (1, q.rows):
+            raise ValueError(f"{name}.gscale: expected 1 or {q.rows} values")
+    return q
+
+
+def _fp4_device(*items):
+    """The one device of the operands, made current for the call (a kernel is launched on the
+    device and on the current stream of its operands)."""
+    devs = {t.device for t in items if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"operands on different devices: {sorted(map(str, devs))}")
+    return torch.cuda.device(devs.pop())
+
+
+def _workspace(workspace, need: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return _fp4_tensor(workspace, "workspace", (torch.uint8,))
+
+
+def qlora_fp4_quantize(X: torch.Tensor, fmt: int = FP4_NVFP4,
+                       out: FP4Matrix | None = None) -> FP4Matrix:
+    """X [rows, cols] (fp32 or bf16, CUDA, contiguous) to microscaled form, each row by
+    itself; cols % 32 == 0."""
+    _fp4_tensor(X, "X", _FP4_DTYPES)
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    rows, cols = X.shape
+    q = out if out is not None else FP4Matrix.empty(rows, cols, fmt, X.device)
+    if (q.rows, q.cols, q.fmt) != (rows, cols, fmt):
+        raise ValueError("out: another shape or format than X")
+    _fp4_matrix(q, "out")
+    if fmt == FP4_NVFP4 and (q.gscale is None or q.gscale.numel() != rows):
+        raise ValueError("out.gscale: expected one value per row")
+    with _fp4_device(X, q.codes, q.scales, q.gscale):
+        _check(lib().qlora_fp4_quantize(_ptr(X), _FP4_DTYPES[X.dtype], rows, cols, fmt,
+                                        _ptr(q.codes), _ptr(q.scales), _ptr(q.gscale), _stream()),
+               "qlora_fp4_quantize")
+    return q
+
+
+def qlora_fp4_quantize_weight(W: torch.Tensor, fmt: int = FP4_NVFP4, transposed: bool = True,
+                              out: FP4Weight | None = None,
+                              workspace: torch.Tensor | None = None) -> FP4Weight:
+    """W [n_out, k_in] (fp32 or bf16, CUDA, contiguous, multiples of 32) with square blocks;
+    transposed: also the copy that the backward reads."""
+    _fp4_tensor(W, "W", _FP4_DTYPES)
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
+    n, k = W.shape
+    if out is None:
+        w = FP4Matrix.empty(n, k, fmt, W.device, gscale_rows=1)
+        wt = FP4Matrix.empty(k, n, fmt, W.device, gscale_rows=1) if transposed else None
+        out = FP4Weight(w, wt)
+    w, wt = out.w, out.wt if transposed else None
+    if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
+            wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):
+        raise ValueError("out: another shape or format than W")
+    _fp4_matrix(w, "out.w")
+    if wt is not None:
+        _fp4_matrix(wt, "out.wt")
+        wt.gscale = w.gscale  # one value for both
+    if fmt == FP4_NVFP4 and (w.gscale is None or w.gscale.numel() != 1):
+        raise ValueError("out.w.gscale: expected one value")
+    ws = _workspace(workspace, int(lib().qlora_fp4_quantize_weight_workspace_size()), W.device)
+    with _fp4_device(W, w.codes, w.scales, w.gscale, ws, *([wt.codes, wt.scales] if wt else [])):
+        _check(lib().qlora_fp4_quantize_weight(
+            _ptr(W), _FP4_DTYPES[W.dtype], n, k, fmt, _ptr(w.codes), _ptr(w.scales),
+            _ptr(w.gscale), _ptr(wt.codes if wt else None), _ptr(wt.scales if wt else None),
+            _ptr(ws), ws.numel(), _stream()), "qlora_fp4_quantize_weight")
+    return FP4Weight(w, wt)
+
+
+def qlora_fp4_dequant(q: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of a microscaled matrix [rows, cols], bf16 or fp32."""
+    _fp4_matrix(q, "q")
+    if out is None:
+        out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
+    _fp4_tensor(out, "out", _FP4_DTYPES, (q.rows, q.cols))
+    with _fp4_device(q.codes, q.scales, q.gscale, out):
+        _check(lib().qlora_fp4_dequant(q.c_struct(), _FP4_DTYPES[out.dtype], _ptr(out), _stream()),
+               "qlora_fp4_dequant")
+    return out
+
+
+def qlora_fp4_matmul(a: FP4Matrix, b: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """a b^T [a.rows, b.rows], bf16 or fp32; both operands of one format, b.rows % 8 == 0."""
+    _fp4_matrix(a, "a"), _fp4_matrix(b, "b")
+    if out is None:
+        out = torch.empty(a.rows, b.rows, dtype=dtype, device=a.codes.device)
+    _fp4_tensor(out, "out", _FP4_DTYPES, (a.rows, b.rows))
+    with _fp4_device(a.codes, a.scales, a.gscale, b.codes, b.scales, b.gscale, out):
+        _check(lib().qlora_fp4_matmul(a.c_struct(), b.c_struct(), _FP4_DTYPES[out.dtype],
+                                      _ptr(out), _stream()), "qlora_fp4_matmul")
+    return out
+
+
+def qlora_fp4_linear_fwd_workspace_size(M: int, n_out: int, k_in: int, r: int,
+                                        fmt: int = FP4_NVFP4) -> int:
+    return int(lib().qlora_fp4_linear_fwd_workspace_size(M, n_out, k_in, r, fmt))
+
+
+def qlora_fp4_linear_bwd_workspace_size(M: int, n_out: int, k_in: int, r: int,
+                                        fmt: int = FP4_NVFP4) -> int:
+    return int(lib().qlora_fp4_linear_bwd_workspace_size(M, n_out, k_in, r, fmt))
+
+
+def qlora_fp4_linear_fwd(X: torch.Tensor, w: FP4Weight, A: torch.Tensor, B: torch.Tensor,
+                         scale: float, save_T: bool = True, Y: torch.Tensor | None = None,
+                         T: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Y = bf16(q(X) W^T + scale (X A) B) on a microscaled weight. Returns (Y, T) with
+    T = X A (fp32) or None."""
+    q = _fp4_matrix(w.w, "w")
+    bf, dev = (torch.bfloat16,), X.device
+    M, r = X.shape[0], A.shape[1]
+    _fp4_tensor(X, "X", bf, (M, q.cols)), _fp4_tensor(A, "A", bf, (q.cols, r))
+    _fp4_tensor(B, "B", bf, (r, q.rows))
+    Y = Y if Y is not None else torch.empty(M, q.rows, dtype=torch.bfloat16, device=dev)
+    _fp4_tensor(Y, "Y", bf, (M, q.rows))
+    if save_T:
+        T = T if T is not None else torch.empty(M, r, dtype=torch.float32, device=dev)
+        _fp4_tensor(T, "T", (torch.float32,), (M, r))
+    else:
+        T = None
+    with _fp4_device(X, q.codes, q.scales, q.gscale, A, B, Y, T, workspace):
+        ws = _workspace(workspace, qlora_fp4_linear_fwd_workspace_size(M, q.rows, q.cols, r, q.fmt),
+                        dev)
+        _check(lib().qlora_fp4_linear_fwd(_ptr(X), M, q.c_struct(), _ptr(A), _ptr(B), r,
+                                          float(scale), _ptr(Y), _ptr(T), _ptr(ws), ws.numel(),
+                                          _stream()), "qlora_fp4_linear_fwd")
+    return Y, T
+
+
+def qlora_fp4_linear_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor | None, w: FP4Weight,
+                         A: torch.Tensor, B: torch.Tensor, scale: float, need_dX: bool = True,
+                         dX: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                         dB: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Gradients (dX bf16 or None, dA fp32 [K, r], dB fp32 [r, N]) of qlora_fp4_linear_fwd;
+    W is frozen and needs its transposed copy."""
+    if w.wt is None:
+        raise ValueError("w.wt: the backward reads the transposed copy")
+    q = _fp4_matrix(w.wt, "w.wt")
+    K, N, bf, f32, dev = q.rows, q.cols, (torch.bfloat16,), (torch.float32,), X.device
+    M, r = X.shape[0], A.shape[1]
+    _fp4_tensor(dY, "dY", bf, (M, N)), _fp4_tensor(X, "X", bf, (M, K))
+    _fp4_tensor(A, "A", bf, (K, r)), _fp4_tensor(B, "B", bf, (r, N))
+    if T is not None:
+        _fp4_tensor(T, "T", f32, (M, r))
+    if need_dX:
+        dX = dX if dX is not None else torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+        _fp4_tensor(dX, "dX", bf, (M, K))
+    else:
+        dX = None
+    dA = dA if dA is not None else torch.empty(K, r, dtype=torch.float32, device=dev)
+    dB = dB if dB is not None else torch.empty(r, N, dtype=torch.float32, device=dev)
+    _fp4_tensor(dA, "dA", f32, (K, r)), _fp4_tensor(dB, "dB", f32, (r, N))
+    with _fp4_device(dY, X, T, q.codes, q.scales, q.gscale, A, B, dX, dA, dB, workspace):
+        ws = _workspace(workspace, qlora_fp4_linear_bwd_workspace_size(M, N, K, r, q.fmt), dev)
+        _check(lib().qlora_fp4_linear_bwd(_ptr(dY), _ptr(X), _ptr(T), M, q.c_struct(), _ptr(A),
+                                          _ptr(B), r, float(scale), _ptr(dX), _ptr(dA), _ptr(dB),
+                                          _ptr(ws), ws.numel(), _stream()), "qlora_fp4_linear_bwd")
+    return dX, dA, dB

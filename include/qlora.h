@@ -387,6 +387,134 @@ qlora_status qlora_linear_bwd_shard(const uint16_t *dY, const uint16_t *X, const
 qlora_status qlora_f32_to_bf16(const float *src, uint16_t *dst, int64_t n, void *stream);
 
 /*
+ * ---- Microscaled 4-bit floating point (MXFP4, NVFP4) ----
+ * A 4-bit storage that the tensor cores multiply without expanding it: E2M1 codes (0, .5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives) with one scale per block of a row.
+ *   QLORA_FP4_MX  blocks of 32, scale 2^(byte - 127) (E8M0; byte 255 is NaN)
+ *   QLORA_FP4_NV  blocks of 16, scale E4M3 (bytes 0..0x7F; 0x7F is NaN), and an fp32 gscale
+ *                 per matrix or per row
+ * value(i, j) = e2m1(code) * scale(i, j / block) * gscale. (The formats are those of the OCP
+ * microscaling specification and of NVIDIA's public NVFP4 description; the method's pages
+ * compare NF4 with a 4-bit float without defining one.)
+ *
+ * Storage of a matrix [rows, cols], cols % 32 == 0:
+ *   codes  uint8 [rows, cols/2]  the even column in the low nibble
+ *   scales uint8, qlora_fp4_scales_bytes(): tiles of 128 rows x 4 blocks, 512 bytes each,
+ *          ordered by row tile, then along the row; byte of (row, block) in its tile:
+ *          (row % 32) * 16 + (row % 128) / 32 * 4 + block % 4. Blocks past the last column
+ *          inside the last tile hold 0; bytes of rows past the last are unspecified.
+ *   gscale fp32 [gscale_rows], gscale_rows = 1 or rows; NULL stands for 1
+ */
+typedef enum { QLORA_FP4_MX = 0, QLORA_FP4_NV = 1 } qlora_fp4_format;
+
+typedef struct {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const float *gscale;  /* or NULL */
+  int64_t gscale_rows;  /* 1 or rows (ignored when gscale is NULL) */
+  int64_t rows, cols;
+  int32_t format;       /* qlora_fp4_format */
+} qlora_fp4_matrix;
+
+/* Bytes of the tiled scale array of a rows x cols matrix (0 for sizes that are not allowed). */
+size_t qlora_fp4_scales_bytes(int64_t rows, int64_t cols, int32_t format);
+
+/*
+ * qlora_fp4_quantize: X [rows, cols] (device, fp32 or bf16, row-major) to microscaled form,
+ * row by row: a row's result depends on that row alone (activations and gradients).
+ *   MX: e = floor(log2 amax) - 2, clamped to [-127, 127] (-127 for amax = 0), over the block's
+ *       largest magnitude amax; scale byte e + 127; code = e2m1(x / 2^e)
+ *   NV: gscale[row] = 2^e, e >= -126 the smallest with rowmax <= 2688 * 2^e (2688 = 6 * 448),
+ *       1 for a row of zeros; scale byte c = e4m3(amax / gscale / 6);
+ *       code = e2m1(x / gscale / c), 0 where c = 0
+ * e2m1() and e4m3() round to nearest, ties to even, and saturate (6 and 448); codes and
+ * scales are exactly those of these formulas in real arithmetic (x / gscale below fp32's
+ * smallest normal number counts as 0). The gscale is a power of two so that dividing by it is
+ * exact: it only places the E4M3 range, whose relative precision does not depend on it.
+ * A NaN or an infinity makes its block's scale NaN and that block's codes 0, and does not
+ * enter rowmax.
+ *   codes, scales as above; gscale fp32 [rows] (NV; not used and may be NULL for MX)
+ * rows == 0 enqueues nothing. Errors: QLORA_ERR_SHAPE unless 0 <= rows < 2^31 - 256,
+ * 32 <= cols < 2^31, cols % 32 == 0 and rows * cols <= 2^40; QLORA_ERR_INVALID_ARG for a NULL
+ * pointer, an unknown dtype or format; QLORA_ERR_ALIGN unless the pointers are 16-byte aligned.
+ */
+qlora_status qlora_fp4_quantize(const void *X, qlora_dtype x_dtype, int64_t rows, int64_t cols,
+                                int32_t format, uint8_t *codes, uint8_t *scales, float *gscale,
+                                void *stream);
+
+/* Device bytes of workspace qlora_fp4_quantize_weight needs. */
+size_t qlora_fp4_quantize_weight_workspace_size(void);
+
+/*
+ * qlora_fp4_quantize_weight: W [n_out, k_in] (device, fp32 or bf16) with one scale per square
+ * of 32 x 32 (MX) or 16 x 16 (NV) values and one gscale for the matrix, in the formulas of
+ * qlora_fp4_quantize (amax over the square, rowmax over the matrix). Squares are blocks in
+ * both directions, so W and its transpose hold the same values: the forward reads w, the
+ * gradient of the input reads wt.
+ *   codes, scales       W [n_out, k_in]
+ *   t_codes, t_scales   W^T [k_in, n_out], both NULL to leave it out
+ *   gscale fp32 [1]     of both (NV; may be NULL for MX)
+ * Errors: QLORA_ERR_SHAPE unless n_out and k_in are multiples of 32, at least 32, n_out <= 2^22 - 64
+ * and n_out * k_in <= 2^40; otherwise those of qlora_fp4_quantize and QLORA_ERR_WORKSPACE.
+ */
+qlora_status qlora_fp4_quantize_weight(const void *W, qlora_dtype w_dtype, int64_t n_out,
+                                       int64_t k_in, int32_t format, uint8_t *codes,
+                                       uint8_t *scales, float *gscale, uint8_t *t_codes,
+                                       uint8_t *t_scales, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
+ * qlora_fp4_dequant: out [rows, cols] (device, fp32 or bf16) = the values of q:
+ * fl32(e2m1 * scale * gscale), the first product exact, rounded once more for bf16. A NaN
+ * scale reads as NaN. rows == 0 enqueues nothing.
+ */
+qlora_status qlora_fp4_dequant(qlora_fp4_matrix q, qlora_dtype out_dtype, void *out, void *stream);
+
+/*
+ * qlora_fp4_matmul: out [a.rows, b.rows] (device, fp32 or bf16, row-major) = a b^T, products
+ * and block scales exact, sums in fp32, then the two gscales, one rounding to bf16.
+ * Errors: QLORA_ERR_SHAPE unless a.cols == b.cols, b.rows >= 8 and b.rows % 8 == 0;
+ * QLORA_ERR_INVALID_ARG when the formats differ. a.rows == 0 enqueues nothing. No workspace.
+ */
+qlora_status qlora_fp4_matmul(qlora_fp4_matrix a, qlora_fp4_matrix b, qlora_dtype out_dtype,
+                              void *out, void *stream);
+
+/* Device bytes of workspace qlora_fp4_linear_fwd needs. */
+size_t qlora_fp4_linear_fwd_workspace_size(int64_t M, int64_t n_out, int64_t k_in, int r,
+                                           int32_t format);
+
+/*
+ * qlora_fp4_linear_fwd: qlora_linear_fwd on a microscaled weight,
+ *   Y [M, N] bf16 = bf16(q(X) W^T + scale (X A) B),   T_save [M, r] fp32 or NULL = X A
+ * q() is qlora_fp4_quantize in the weight's format; the LoRA term sees the 16-bit X. w is
+ * [N, K] of qlora_fp4_quantize_weight (or any with one gscale), N % 32 == 0. Other arguments,
+ * layouts and errors as qlora_linear_fwd. The LoRA term is carried in units of the gscales:
+ * |scale T B| / (gscale of the row * gscale of w) has to stay in fp32's range.
+ */
+qlora_status qlora_fp4_linear_fwd(const uint16_t *X, int64_t M, qlora_fp4_matrix w,
+                                  const uint16_t *A, const uint16_t *B, int r, float scale,
+                                  uint16_t *Y, float *T_save, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Device bytes of workspace qlora_fp4_linear_bwd needs. */
+size_t qlora_fp4_linear_bwd_workspace_size(int64_t M, int64_t n_out, int64_t k_in, int r,
+                                           int32_t format);
+
+/*
+ * qlora_fp4_linear_bwd: gradients of qlora_fp4_linear_fwd, rounding to 4 bits passed through
+ * (straight-through), W frozen:
+ *   G = dY B^T,  dX = bf16(q(dY) W + scale G A^T),  dA = scale X^T G,  dB = scale T^T dY
+ * wt is W^T [K, N] of qlora_fp4_quantize_weight. q() rounds dY to nearest in blocks along N,
+ * for the large product only; G, dA and dB see the 16-bit dY. Other arguments, layouts and
+ * errors as qlora_linear_bwd.
+ */
+qlora_status qlora_fp4_linear_bwd(const uint16_t *dY, const uint16_t *X, const float *T_saved,
+                                  int64_t M, qlora_fp4_matrix wt, const uint16_t *A,
+                                  const uint16_t *B, int r, float scale, uint16_t *dX, float *dA,
+                                  float *dB, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
  * qlora_selftest_wait_timeout: a test hook for the failure path that every kernel's
  * bounded waits share (not part of the method). Enqueues on `stream` one small kernel
  * whose only wait, on an mbarrier that nothing arrives at, runs out after the library's

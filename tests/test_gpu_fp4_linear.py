@@ -1,0 +1,255 @@
+"""GPU parity of the microscaled 4-bit product and of the linear layer on it against the fp64
+oracle.
+
+Tolerances, element by element. u = 2^-23 bounds the relative error of one fp32 addition,
+rounded or truncated. A product of K values is a chain of K / 64 additions into the
+accumulator, each of which may also drop bits below u of the running sum of magnitudes S, so
+its error is at most (K / 64 + 8) u S; a rank-r product (K / 16 steps, then at most 64 partial
+sums) at most (K / 16 + 80) u S. A bf16 hi + lo pair keeps 2^-16 of its value. bf16 outputs add
+half a bf16 step, 2^-8 of the value, and the errors of what is rounded."""
+import numpy as np
+import pytest
+import torch
+
+from bit_nf4_quantized_unpack_b200 import qlora
+from oracle import fp4_oracle as F
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [qlora.FP4_MXFP4, qlora.FP4_NVFP4]
+U, PAIR, BF16 = 2.0 ** -23, 2.0 ** -16, 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+    yield
+    assert qlora.qlora_device_error() == 0
+
+
+def normal(seed, *shape, std=1.0):
+    g = np.random.default_rng(seed)
+    return torch.from_numpy(g.normal(0, std, shape)).to(torch.bfloat16)
+
+
+def within(got, want, tol, what):
+    got, tol = got.detach().double().cpu().numpy(), np.broadcast_to(tol, want.shape)
+    assert got.shape == want.shape and np.isfinite(got).all(), what
+    bad = np.abs(got - want) > tol
+    i = np.unravel_index(np.argmax(np.abs(got - want) - tol), want.shape) if want.size else None
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, worst at {i}: {got[i]} for {want[i]}, tol {tol[i]}"
+
+
+def product_tol(a, b):
+    return (a.shape[1] / 64 + 8) * U * (np.abs(a) @ np.abs(b).T)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [
+    (1, 8, 32), (2, 136, 64), (31, 128, 96), (32, 256, 256), (33, 1000, 288), (64, 40, 1056),
+    (65, 264, 4096), (128, 128, 512), (129, 520, 544), (256, 256, 1024), (300, 1000, 1056),
+    (513, 384, 160), (1, 4096, 11008), (16, 4096, 4096), (700, 2056, 2048)])
+def test_matmul(M, N, K, fmt):
+    a, b = normal(M + K, M, K).cuda(), normal(N, N, K, std=0.02).cuda()
+    a[M // 2] = 0.0
+    qa, qb = qlora.qlora_fp4_quantize(a, fmt), qlora.qlora_fp4_quantize(b, fmt)
+    va, vb = (F.dequant(F.quantize(t.double().cpu().numpy(), fmt)) for t in (a, b))
+    want, tol = va @ vb.T, product_tol(va, vb)
+    big = torch.full((M + 2, N), 7.0, device="cuda")
+    got = qlora.qlora_fp4_matmul(qa, qb, out=big[1:M + 1])
+    within(got, want, tol, "fp32")
+    assert (big[0] == 7).all() and (big[M + 1] == 7).all()
+    got16 = qlora.qlora_fp4_matmul(qa, qb)
+    within(got16, want, tol + BF16 * (np.abs(want) + tol), "bf16")
+    assert torch.equal(got, qlora.qlora_fp4_matmul(qa, qb, torch.float32))  # the same bits again
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_matmul_reads_every_scale_in_its_place(fmt):
+    """One-hot codes under scales that all differ: each output is one product of a code and two
+    scales, exact in fp32."""
+    g = np.random.default_rng(1)
+    b = F.BLOCK[fmt]
+    for M, N, K in ((40, 136, 416), (300, 264, 288)):
+        def one_hot(rows):
+            codes = np.zeros((rows, K), np.uint8)
+            codes[np.arange(rows), g.integers(0, K, rows)] = g.integers(1, 16, rows)
+            lo, hi = (100, 150) if fmt == F.MX else (1, 127)
+            return {"codes": codes, "bytes": g.integers(lo, hi, (rows, K // b)).astype(np.uint8),
+                    "g": np.ones(1), "fmt": fmt}
+        def full(rows):
+            q = one_hot(rows)
+            q["codes"] = np.full((rows, K), 2, np.uint8)
+            return q
+        for ra, rb in ((one_hot(M), full(N)), (full(M), one_hot(N))):
+            qa, qb = (qlora.FP4Matrix(torch.from_numpy(F.pack(r["codes"])).cuda(),
+                                      torch.from_numpy(F.store_scales(r["bytes"])).cuda(), None,
+                                      *r["codes"].shape, fmt) for r in (ra, rb))
+            want = F.dequant(ra) @ F.dequant(rb).T
+            got = qlora.qlora_fp4_matmul(qa, qb, torch.float32)
+            assert np.array_equal(got.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [5, 300])
+def test_matmul_nan_blocks_and_gscales(M, fmt):
+    """A NaN block reaches the outputs of its row (column) alone; gscales per row and single."""
+    K, N = 544, 136
+    a, b = normal(3, M, K).cuda(), normal(4, N, K).cuda()
+    a[2, 100], b[7, 540] = float("nan"), float("inf")
+    qa, qb = qlora.qlora_fp4_quantize(a, fmt), qlora.qlora_fp4_quantize(b, fmt)
+    out = qlora.qlora_fp4_matmul(qa, qb, torch.float32)
+    nan = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    nan[2], nan[:, 7] = True, True
+    assert torch.equal(torch.isnan(out), nan)
+    ga = torch.rand(M, device="cuda") + 0.5
+    gb = torch.rand(1, device="cuda") + 0.5
+    bare = [qlora.FP4Matrix(q.codes, q.scales, None, q.rows, q.cols, fmt) for q in (qa, qb)]
+    base = qlora.qlora_fp4_matmul(*bare, torch.float32)
+    got = qlora.qlora_fp4_matmul(qlora.FP4Matrix(qa.codes, qa.scales, ga, M, K, fmt),
+                                 qlora.FP4Matrix(qb.codes, qb.scales, gb, N, K, fmt), torch.float32)
+    want = (base * gb) * ga[:, None]
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+
+
+def layer(seed, M, N, K, r, fmt):
+    W, A, B = normal(seed, N, K, std=0.02), normal(seed + 1, K, r, std=0.02), normal(seed + 2, r, N, std=0.02)
+    X, dY = normal(seed + 3, M, K), normal(seed + 4, M, N)
+    if M > 4:
+        X[M // 2] = 0.0
+        dY[M - 1] = 0.0
+    return W, A, B, X, dY
+
+
+def check_layer(M, N, K, r, fmt, scale=0.5, saved_T=True):
+    W, A, B, X, dY = layer(M + N + K, M, N, K, r, fmt)
+    q = qlora.qlora_fp4_quantize_weight(W.cuda(), fmt)
+    Xc, Ac, Bc, dYc = X.cuda(), A.cuda(), B.cuda(), dY.cuda()
+    Y, T = qlora.qlora_fp4_linear_fwd(Xc, q, Ac, Bc, scale)
+    dX, dA, dB = qlora.qlora_fp4_linear_bwd(dYc, Xc, T if saved_T else None, q, Ac, Bc, scale)
+    A64, B64, X64, dY64 = (t.double().numpy() for t in (A, B, X, dY))
+    w, _ = F.quantize_weight(W.double().numpy(), fmt)
+    Y64, T64 = F.linear_forward(X64, w, A64, B64, scale)
+    dX64, dA64, dB64 = F.linear_backward(dY64, X64, w, A64, B64, scale)
+    a = np.abs
+    Wv, Xq, dYq = F.dequant(w), F.dequant(F.quantize(X64, fmt)), F.dequant(F.quantize(dY64, fmt))
+    T_tol = (K / 16 + 80) * U * (a(X64) @ a(A64))
+    within(T, T64, T_tol, "T")
+    lora = lambda v, tol, m: abs(scale) * ((PAIR + 16 * U) * (a(v) @ a(m)) + tol @ a(m))
+    y_tol = product_tol(Xq, Wv) + lora(T64, T_tol, B64)
+    within(Y, Y64, y_tol + BF16 * (a(Y64) + y_tol), "Y")
+    G64 = dY64 @ B64.T
+    G_tol = (N / 16 + 80) * U * (a(dY64) @ a(B64).T)
+    x_tol = product_tol(dYq, Wv.T) + lora(G64, G_tol, A64.T)
+    within(dX, dX64, x_tol + BF16 * (a(dX64) + x_tol), "dX")
+    steps = (M / 16 + 80) * U + PAIR
+    within(dA, dA64, abs(scale) * (steps * (a(X64).T @ a(G64)) + a(X64).T @ G_tol), "dA")
+    within(dB, dB64, abs(scale) * (steps * (a(T64).T @ a(dY64)) + T_tol.T @ a(dY64)), "dB")
+    return q, (Xc, Ac, Bc, dYc), (Y, T, dX, dA, dB)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,r", [
+    (1, 32, 32, 8), (1, 1024, 4096, 16), (5, 160, 96, 8), (16, 512, 1024, 64), (33, 416, 288, 24),
+    (64, 256, 544, 40), (128, 288, 256, 16), (129, 352, 1056, 8), (300, 384, 640, 64), (520, 1056, 512, 32)])
+def test_linear(M, N, K, r, fmt):
+    check_layer(M, N, K, r, fmt)
+
+
+def test_linear_recomputes_T():
+    check_layer(70, 160, 320, 16, qlora.FP4_NVFP4, saved_T=False)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gradients_against_differences(fmt):
+    """The layer without its roundings is linear in A and in B and, on the 4-bit grid, in X: the
+    difference of two outputs along a direction is the gradient's inner product with it. The
+    outputs differenced here are the oracle's, the gradients the kernels'."""
+    M, N, K, r, scale = 24, 64, 96, 8, 0.5
+    q, (X, A, B, dY), (_, _, dX, dA, dB) = check_layer(M, N, K, r, fmt)
+    Wv = qlora.qlora_fp4_dequant(q.w, torch.float32).double().cpu().numpy()
+    dYq = qlora.qlora_fp4_dequant(qlora.qlora_fp4_quantize(dY, fmt), torch.float32).double().cpu().numpy()
+    X, A, B, dY = (t.double().cpu().numpy() for t in (X, A, B, dY))
+    f = lambda X_, A_, B_: np.sum((X_ @ Wv.T) * dYq) + scale * np.sum((X_ @ A_ @ B_) * dY)
+    g = np.random.default_rng(3)
+    for grad, i, rel in ((dX, 0, BF16), (dA, 1, 2.0 ** -14), (dB, 2, 2.0 ** -14)):
+        grad = grad.double().cpu().numpy()
+        V = g.normal(0, 1, grad.shape)
+        hi, lo = [X, A, B], [X, A, B]
+        hi[i], lo[i] = hi[i] + V, lo[i] - V
+        assert abs((f(*hi) - f(*lo)) / 2 - np.sum(grad * V)) <= rel * np.sum(np.abs(grad * V)) + 1e-6
+
+
+def test_empty_batch_and_partial_outputs():
+    W, A, B, X, dY = (t.cuda() for t in layer(9, 20, 64, 96, 8, 1))
+    q = qlora.qlora_fp4_quantize_weight(W)
+    Y, T = qlora.qlora_fp4_linear_fwd(X[:0], q, A, B, 1.0)
+    assert Y.shape == (0, 64) and T.shape == (0, 8)
+    dX, dA, dB = qlora.qlora_fp4_linear_bwd(dY[:0], X[:0], None, q, A, B, 1.0)
+    assert dX.shape == (0, 96) and not dA.any() and not dB.any()
+    full = qlora.qlora_fp4_linear_bwd(dY, X, None, q, A, B, 1.0)
+    none, dA, dB = qlora.qlora_fp4_linear_bwd(dY, X, None, q, A, B, 1.0, need_dX=False)
+    assert none is None and torch.equal(dA, full[1]) and torch.equal(dB, full[2])
+    Y1, none = qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0, save_T=False)
+    assert none is None and torch.equal(Y1, qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0)[0])
+
+
+def test_streams_and_graphs():
+    """The same bits on another stream, in a captured and replayed graph with new inputs, and
+    from two streams at once."""
+    for M in (3, 200):
+        W, A, B, X, dY = (t.cuda() for t in layer(11, M, 256, 320, 16, 1))
+        q = qlora.qlora_fp4_quantize_weight(W)
+
+        def step(x, dy):
+            y, t = qlora.qlora_fp4_linear_fwd(x, q, A, B, 0.5)
+            return (y, t) + qlora.qlora_fp4_linear_bwd(dy, x, t, q, A, B, 0.5)
+        want, X2, dY2 = step(X, dY), X.flip(0).contiguous(), dY.flip(0).contiguous()
+        want2 = step(X2, dY2)
+        torch.cuda.synchronize()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        got = {}
+        for _ in range(3):
+            for name, s, args in (("a", s1, (X, dY)), ("b", s2, (X2, dY2))):
+                with torch.cuda.stream(s):
+                    got[name] = step(*args)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got["a"], want))
+        assert all(torch.equal(x, y) for x, y in zip(got["b"], want2))
+        bx, bdy = X.clone(), dY.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(bx, bdy)
+        for src, ref in (((X2, dY2), want2), ((X, dY), want)):
+            bx.copy_(src[0]), bdy.copy_(src[1])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(out, ref))
+
+
+def test_training_step_on_a_microscaled_weight():
+    """The operators together: lay the weight out, forward, backward, optimizer step, and the
+    next forward on the updated adapter."""
+    from oracle import adamw_oracle as AW
+    W, A, B, X, dY = layer(21, 96, 128, 160, 8, 1)
+    scale = 0.25
+    q = qlora.qlora_fp4_quantize_weight(W.cuda())
+    p0 = torch.cat([A.reshape(-1), B.reshape(-1)]).float()
+    p, pb = p0.cuda(), torch.empty(p0.numel(), dtype=torch.bfloat16, device="cuda")
+    state = torch.zeros(qlora.qlora_adamw_state_bytes(p.numel(), 8), dtype=torch.uint8, device="cuda")
+    Y, T = qlora.qlora_fp4_linear_fwd(X.cuda(), q, A.cuda(), B.cuda(), scale)
+    _, dA, dB = qlora.qlora_fp4_linear_bwd(dY.cuda(), X.cuda(), T, q, A.cuda(), B.cuda(), scale)
+    g = torch.cat([dA.reshape(-1), dB.reshape(-1)])
+    qlora.qlora_adamw_step(p, g, state, 1, lr=1e-2, p_bf16=pb)
+    A1, B1 = pb[:160 * 8].view(160, 8), pb[160 * 8:].view(8, 128)
+    Y1, _ = qlora.qlora_fp4_linear_fwd(X.cuda(), q, A1, B1, scale)
+    want, _, _ = AW.adamw_step_8bit(p0.numpy(), g.cpu().numpy(), AW.zero_state_8bit(p0.numel()), lr=1e-2,
+                                    beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1)
+    assert np.array_equal(p.cpu().numpy(), want)
+    w, _ = F.quantize_weight(W.double().numpy(), 1)
+    Y64, T64 = F.linear_forward(X.double().numpy(), w, A1.double().cpu().numpy(),
+                                B1.double().cpu().numpy(), scale)
+    tol = 1e-4 * np.abs(T64) @ np.abs(B1.double().cpu().numpy()) + 1e-4 * np.abs(X.double().numpy()) @ np.abs(F.dequant(w)).T
+    within(Y1, Y64, tol + BF16 * (np.abs(Y64) + tol), "Y after the step")
+    assert not torch.equal(Y, Y1)
