@@ -276,10 +276,352 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ pair kernel
+// A persistent CTA pair per two SMs; a tile is 256 weight rows x 256 tokens. Each CTA holds 128
+// weight rows of the operand, 128 tokens of the other, its rows' scales and all 256 tokens'
+// scales, and accumulates its 128 rows x 256 tokens in its own tensor memory.
+//
+// Tensor memory: two 256-column accumulators used in turn and two sets of scale columns. They
+// do not fit side by side (2 * 256 + 2 * 48 > 512), so the accumulators share the columns
+// [160, 256): the epilogue reads those first and then lets the next tile's MMAs start, while
+// it goes on with the other 160 columns.
+//
+// Warp 0: TMA, warp 1: MMA (in the leader) and tensor memory, warps 2-9: epilogue, two warps
+// for each quarter of the lanes.
+constexpr int kPairThreads = 320;
+constexpr int kPairStages = 5;
+constexpr int kPairTile = 256;                // weight rows and tokens of a tile
+constexpr uint32_t kPairQBytes = 128 * 128;
+constexpr uint32_t kPairSf = 4 * kSfTile;     // scales of 128 rows and one step (NVFP4)
+constexpr uint32_t kPairStage = kPBytes + kPairQBytes + 3 * kPairSf;
+constexpr uint32_t kPairEpi = 8 * 2 * 32 * 32 * 2;
+constexpr uint32_t kPairSmem = 1024 + kPairStages * kPairStage + kPairEpi + 256;
+static_assert(kPairSmem <= 227 * 1024, "shared memory per CTA");
+constexpr uint32_t kAcc1 = 160;               // first column of the second accumulator
+constexpr uint32_t kSfCol = 416;              // first scale column; sets of 48
+constexpr int kEpiWarps = 8;
+
+struct PairTile {
+  int64_t p0, q0;
+};
+// Tiles in groups of eight token tiles, so that the tiles in flight at one time form a block
+// that shares operands in L2.
+__device__ __forceinline__ PairTile pair_tile(int t, int p_tiles, int q_tiles) {
+  constexpr int kGroup = 8;
+  const int per = kGroup * p_tiles;
+  const int g = t / per, in = t - g * per;
+  const int width = min(kGroup, q_tiles - g * kGroup);
+  return {static_cast<int64_t>(in / width) * kPairTile,
+          static_cast<int64_t>(g * kGroup + in % width) * kPairTile};
+}
+
+template <Fp4 F, bool OUT_F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_fp4_gemm_pair(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_sp, const __grid_constant__ CUtensorMap tm_sq,
+                    const __grid_constant__ CUtensorMap tm_ext_p,
+                    const __grid_constant__ CUtensorMap tm_ext_q,
+                    const __grid_constant__ CUtensorMap tm_out, const Fp4Args args) {
+  constexpr int S = kPairStages;
+  constexpr int kTileStep = kStepCols / kFp4TileCols<F>;  // scale tiles per step: 2 or 4
+  constexpr int kMmaTile = 4 / kTileStep;                 // MMAs per scale tile: 2 or 1
+  constexpr uint32_t kSfBytes = kTileStep * kSfTile;      // of 128 rows and one step
+  constexpr uint32_t kStepTx = 2 * (kPBytes + kPairQBytes + 3 * kSfBytes);  // both CTAs
+  constexpr uint32_t kExtTx = 2 * (kPBytes + kPairQBytes);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* p_s = smem;                          // [S][kPBytes]
+  uint8_t* q_s = p_s + S * kPBytes;             // [S][kPairQBytes]
+  uint8_t* epi_s = q_s + S * kPairQBytes;       // [8 warps][2][32][32] bf16
+  uint8_t* sfp_s = epi_s + kPairEpi;            // [S][kPairSf]
+  uint8_t* sfq_s = sfp_s + S * kPairSf;         // [S][2 kPairSf]: two row tiles, kSfBytes each
+  uint64_t* full = reinterpret_cast<uint64_t*>(sfq_s + S * 2 * kPairSf);  // the leader's counts
+  uint64_t* empty = full + S;                   // [S] MMAs reading the slot done (both CTAs)
+  uint64_t* acc_full = empty + S;               // accumulator complete (both CTAs)
+  uint64_t* acc_part = acc_full + 1;            // shared columns read out (the leader's counts)
+  uint64_t* mma_drain = acc_part + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int q_tiles = static_cast<int>((args.Q + kPairTile - 1) / kPairTile);
+  const int tiles = args.p_tiles * q_tiles;
+  const int clusters = gridDim.x / 2, first = blockIdx.x / 2;
+  const int my_tiles = first < tiles ? (tiles - 1 - first) / clusters + 1 : 0;
+  const int ext = args.ext_mmas > 0 ? 2 : 0;  // extension steps, ahead of a tile's others
+  const int total = args.steps + ext;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_part, 2 * kEpiWarps);
+    mbar_init(mma_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait_and_release();
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA: this CTA's share of every step
+    if (lane == 0) {
+      int n = 0;  // steps issued
+      bool ok = true;
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        const PairTile t = pair_tile(first + i * clusters, args.p_tiles, q_tiles);
+        const int p0 = static_cast<int>(t.p0) + 128 * rank, q0 = static_cast<int>(t.q0) + 128 * rank;
+        for (int k = 0; k < total; ++k, ++n) {
+          const int s = n % S;
+          if (n >= S && !mbar_wait(&empty[s], ((n / S) - 1) & 1u, abort_flag)) {
+            record_error(args.err, abort_flag, kErrTimeoutProducer);
+            ok = false;
+            break;
+          }
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          uint8_t *ps = p_s + s * kPBytes, *qs = q_s + s * kPairQBytes;
+          if (k < ext) {  // bf16: hi part, then lo part of the token operand
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], kExtTx);
+            if (args.ext_mn) {
+              tma_load_2d_pair(ps, &tm_ext_p, bar, p0, 0);
+              tma_load_2d_pair(ps + 8192, &tm_ext_p, bar, p0 + 64, 0);
+            } else {
+              tma_load_2d_pair(ps, &tm_ext_p, bar, 0, p0);
+            }
+            tma_load_2d_pair(qs, &tm_ext_q, bar, k * 64, q0);
+          } else {
+            const int step = k - ext;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], kStepTx);
+            tma_load_2d_pair(ps, &tm_p, bar, step * 128, p0);
+            tma_load_2d_pair(qs, &tm_q, bar, step * 128, q0);
+            const int x = step * kTileStep * 64;  // in 8-byte elements
+            tma_load_2d_pair(sfp_s + s * kPairSf, &tm_sp, bar, x, p0 / 128);
+            tma_load_2d_pair(sfq_s + s * 2 * kPairSf, &tm_sq, bar, x, static_cast<int>(t.q0 / 128));
+          }
+        }
+      }
+      // after an abort, the leader lets the copies in flight (both CTAs') land
+      if (*abort_flag && rank == 0)
+        for (int j = max(0, n - S); j < n; ++j) mbar_wait_drain(&full[j % S], (j / S) & 1u);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc_ext = idesc_bf16_f32(kPairTile, kPairTile, args.ext_mn, false);
+      const uint32_t ext_adv = args.ext_mn ? 128u : 2u;
+      int n = 0;
+      bool ok = true;
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        const uint32_t d = tmem + (i & 1) * kAcc1;
+        // The epilogue has the shared columns of tile i - 1 in registers (and, having begun
+        // that tile, all of tile i - 2, which used this accumulator).
+        if (i >= 1) ok = mbar_wait_cluster(acc_part, (i - 1) & 1u, abort_flag);
+        tc_fence_after();
+        for (int k = 0; k < total && ok; ++k) {
+          const int s = n % S;
+          ok = mbar_wait(&full[s], (n / S) & 1u, abort_flag);
+          // The scale columns of this step were last read by the MMAs two steps ago (two sets,
+          // used in turn), and MMAs of different kinds are not ordered with each other: wait
+          // for the completion of step n - 2, or of n - 1 where the kind changes. (At the
+          // start of a tile everything before it is complete: its epilogue has begun.)
+          if (ok && k == ext && ext)
+            ok = mbar_wait(&empty[(n - 1) % S], ((n - 1) / S) & 1u, abort_flag);
+          else if (ok && k >= ext + 2)
+            ok = mbar_wait(&empty[(n - 2) % S], ((n - 2) / S) & 1u, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t pa = smem_u32(p_s + s * kPBytes);
+          const uint64_t dq = smem_desc_sw128(smem_u32(q_s + s * kPairQBytes), 16, 1024);
+          if (k < ext) {
+            const uint64_t dp = args.ext_mn ? smem_desc_sw128(pa, 8192, 1024) : smem_desc_sw128(pa, 16, 1024);
+            for (int kk = 0; kk < args.ext_mmas; ++kk)
+              umma_bf16_pair(d, dp + kk * ext_adv, dq + kk * 2u, idesc_ext, (k | kk) != 0);
+          } else {
+            const uint64_t dp = smem_desc_sw128(pa, 16, 1024);
+            const uint32_t sfp = tmem + kSfCol + (n & 1) * 48, sfq = sfp + 16;
+            const uint32_t sp = smem_u32(sfp_s + s * kPairSf), sq = smem_u32(sfq_s + s * 2 * kPairSf);
+            const int64_t left = args.K - static_cast<int64_t>(k - ext) * kStepCols;
+            const int mmas = left >= kStepCols ? 4 : static_cast<int>((left + 63) / 64);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk >= mmas) break;
+              const int tl = kk / kMmaTile, sub = kk % kMmaTile;
+              if (sub == 0) {
+                tmem_cp_scales_pair(sfp + tl * 4, smem_desc_scales(sp + tl * kSfTile));
+                tmem_cp_scales_pair(sfq + tl * 8, smem_desc_scales(sq + tl * kSfTile));
+                tmem_cp_scales_pair(sfq + tl * 8 + 4, smem_desc_scales(sq + kSfBytes + tl * kSfTile));
+              }
+              umma_fp4_pair<F == Fp4::kMx ? 2 : 4>(
+                  d, dp + kk * 2u, dq + kk * 2u,
+                  idesc_fp4(kPairTile, kPairTile, F == Fp4::kMx, F == Fp4::kMx ? 2 * sub : 0),
+                  sfp + tl * 4, sfq + tl * 8, (k | kk) != 0);
+            }
+          }
+          umma_commit_pair(&empty[s]);
+          if (k == total - 1) umma_commit_pair(acc_full);
+          ++n;
+        }
+      }
+      if (!ok) record_error(args.err, abort_flag, kErrTimeoutMma);
+      umma_commit_pair(mma_drain);
+    }
+  } else {
+    // ------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stage2 = epi_s + (warp - 2) * (2 * 32 * 32 * 2);
+    const uint32_t part_bar = cluster_addr(acc_part, 0);
+    if (lane == 0) tma_prefetch_desc(&tm_out);
+    int chunks = 0;  // stage buffers used
+    for (int i = 0; i < my_tiles; ++i) {
+      const PairTile t = pair_tile(first + i * clusters, args.p_tiles, q_tiles);
+      const int64_t p0 = t.p0 + 128 * rank + quarter * 32;
+      // this warp's four 32-token chunks: the shared columns first. Accumulator 0 shares its
+      // chunks 5-7, accumulator 1 its chunks 0-2.
+      const int shared0 = (i & 1) ? 0 : 5, own0 = (i & 1) ? 3 : 0;
+      const int c0 = shared0 + 2 * half, c1 = half ? own0 + 2 : shared0 + 1;
+      const int c2 = own0 + (half ? 3 : 0), c3 = own0 + (half ? 4 : 1);
+      const int cs[4] = {c0, c1, c2, c3};
+      float gq[4], gp[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        gq[j] = 1.f;
+        gp[j] = 1.f;
+        if (args.gq) gq[j] = __ldg(args.gq + (args.gq_rows ? min(t.q0 + cs[j] * 32 + lane, args.Q - 1) : 0));
+        // rows lane / 4 + 8 j of the quarter (bf16 output), row lane (fp32 output, j = 0)
+        const int64_t row = p0 + (OUT_F32 ? lane : (lane >> 2) + 8 * j);
+        if (args.gp) gp[j] = __ldg(args.gp + (args.gp_rows ? min(row, args.P - 1) : 0));
+      }
+      if (!mbar_wait(acc_full, i & 1u, abort_flag)) {
+        if (!*abort_flag) record_error(args.err, abort_flag, kErrTimeoutEpilogue);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr = tmem + (i & 1) * kAcc1 + (static_cast<uint32_t>(quarter * 32) << 16);
+      // tensor memory -> registers: 32 rows x 32 tokens
+      auto fetch = [&](int c, uint32_t (&v)[32]) {
+        if constexpr (OUT_F32) {
+          tmem_ld_32x32b_x32(taddr + c * 32, v);
+        } else {
+          uint32_t lo[16], hi[16];
+          tmem_ld_16x256b_x4(taddr + c * 32, lo);
+          tmem_ld_16x256b_x4(taddr + (16u << 16) + c * 32, hi);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = lo[j], v[16 + j] = hi[j];
+        }
+      };
+      auto emit = [&](int j, const uint32_t (&v)[32]) {
+        const int64_t q = t.q0 + cs[j] * 32;
+        if (q >= args.Q) return;
+        if constexpr (OUT_F32) {
+          // the chunk fills both stage buffers: stage[token][row]
+          const uint32_t st = smem_u32(stage2);
+          if (chunks >= 1 && lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float x = __uint_as_float(v[k]) * gp[0];
+            if (args.gq) x *= __shfl_sync(~0u, gq[j], k);
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + k * 128 + lane * 4), "f"(x) : "memory");
+          }
+        } else {
+          // bf16 pairs of adjacent tokens, transposed by stmatrix into stage[token][row]: a
+          // token's 64 bytes are four 16-byte groups, group g at slot g ^ ((token >> 1) & 3),
+          // the 64-byte swizzle of the tile store
+          const uint32_t st = smem_u32(stage2) + (chunks & 1) * 2048;
+          if (chunks >= 2 && lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // tokens 8k..8k+7 of the chunk
+            float g0 = 1.f, g1 = 1.f;
+            if (args.gq) {
+              g0 = __shfl_sync(~0u, gq[j], 8 * k + 2 * (lane & 3));
+              g1 = __shfl_sync(~0u, gq[j], 8 * k + 2 * (lane & 3) + 1);
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {  // rows lane / 4 + 8m
+              const int at = (m >> 1) * 16 + 4 * k + (m & 1) * 2;
+              w[m] = pack_bf16x2_rn(__uint_as_float(v[at]) * gp[m] * g0,
+                                    __uint_as_float(v[at + 1]) * gp[m] * g1);
+            }
+            const int tok = 8 * k + (lane & 7);
+            stmatrix_x4_trans(st + tok * 64 + (((lane >> 3) ^ ((tok >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && p0 < args.P) {
+          tma_store_2d(&tm_out, OUT_F32 ? stage2 : stage2 + (chunks & 1) * 2048, static_cast<int>(p0),
+                       static_cast<int>(q));
+          bulk_commit_group();
+        }
+        ++chunks;
+      };
+      uint32_t v0[32], v1[32];
+      fetch(c0, v0);
+      if (half == 0) fetch(c1, v1);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(part_bar);
+      emit(0, v0);
+      if (half != 0) {
+        fetch(c1, v1);
+        tmem_ld_wait();
+      }
+      emit(1, v1);
+      fetch(c2, v0);
+      tmem_ld_wait();
+      emit(2, v0);
+      fetch(c3, v1);
+      tmem_ld_wait();
+      emit(3, v1);
+    }
+    if (lane == 0) bulk_wait_group_all();  // tile stores done before the CTA exits
+  }
+  // The MMAs are complete and the arrivals of the last commits have landed, in each CTA, before
+  // tensor memory and the barriers go.
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    mbar_wait_drain(mma_drain, 0);
+    uint32_t par;
+    for (int s = 0; s < S && !*abort_flag; ++s)
+      if (last_use(my_tiles * total, S, s, par)) mbar_wait_drain(&empty[s], par);
+  }
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  cluster_sync_all();
+}
+
 // ------------------------------------------------------------------ host side
 constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 constexpr CUtensorMapDataType kBf16Map = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B;
+
+// The extension's operand maps (boxes of 128 weight rows, q_box tokens); tp and tq stand in
+// when there is none.
+qlora_status ext_maps(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
+                      uint32_t q_box, CUtensorMap* xp, CUtensorMap* xq) {
+  if (!ext) return QLORA_OK;
+  if (ext->mn_major) QL_MAP(xp, kBf16Map, ext->p, b.rows, ext->r, b.rows * 2, 64, 64, kSw128);
+  else QL_MAP(xp, kBf16Map, ext->p, ext->r, b.rows, ext->r * 2, 64, kPRows, kSw128);
+  QL_MAP(xq, kBf16Map, ext->q, 128, a.rows, 256, 64, q_box, kSw128);
+  return QLORA_OK;
+}
 
 template <Fp4 F, int NT>
 qlora_status run_split(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
@@ -289,11 +631,8 @@ qlora_status run_split(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, con
   QL_MAP(&tq, kU8, a.codes, a.cols / 2, a.rows, a.cols / 2, 128, NT, kSw128);
   xp = tp;
   xq = tq;
-  if (ext) {
-    if (ext->mn_major) QL_MAP(&xp, kBf16Map, ext->p, b.rows, ext->r, b.rows * 2, 64, 64, kSw128);
-    else QL_MAP(&xp, kBf16Map, ext->p, ext->r, b.rows, ext->r * 2, 64, kPRows, kSw128);
-    QL_MAP(&xq, kBf16Map, ext->q, 128, a.rows, 256, 64, NT, kSw128);
-  }
+  qlora_status q = ext_maps(a, b, ext, NT, &xp, &xq);
+  if (q != QLORA_OK) return q;
   auto kern = k_fp4_gemm_split<F, NT>;
   constexpr uint32_t smem = split_smem(NT);
   QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -322,9 +661,44 @@ qlora_status run_split(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, con
 }
 
 template <Fp4 F>
+qlora_status run_pair(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
+                      Fp4Args args, cudaStream_t st) {
+  CUtensorMap tp, tq, sp, sq, xp, xq, to;
+  QL_MAP(&tp, kU8, b.codes, b.cols / 2, b.rows, b.cols / 2, 128, kPRows, kSw128);
+  QL_MAP(&tq, kU8, a.codes, a.cols / 2, a.rows, a.cols / 2, 128, 128, kSw128);
+  // scale tiles as rows of 8-byte elements: 64 per tile
+  constexpr uint32_t box = kStepCols / kFp4TileCols<F> * 64;
+  constexpr CUtensorMapDataType kU64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
+  const uint64_t srow = static_cast<uint64_t>(args.ktiles) * 512;
+  QL_MAP(&sp, kU64, b.scales, srow / 8, (b.rows + 127) / 128, srow, box, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+  QL_MAP(&sq, kU64, a.scales, srow / 8, (a.rows + 127) / 128, srow, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+  xp = tp;
+  xq = tq;
+  qlora_status q = ext_maps(a, b, ext, 128, &xp, &xq);
+  if (q != QLORA_OK) return q;
+  if (args.out_f32)
+    QL_MAP(&to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, args.out, b.rows, a.rows, b.rows * 4, 32, 32,
+           CU_TENSOR_MAP_SWIZZLE_NONE);
+  else
+    QL_MAP(&to, kBf16Map, args.out, b.rows, a.rows, b.rows * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  args.p_tiles = static_cast<int>((b.rows + kPairTile - 1) / kPairTile);
+  const int64_t tiles = static_cast<int64_t>(args.p_tiles) * ((a.rows + kPairTile - 1) / kPairTile);
+  if (tiles > (int64_t{1} << 30)) {
+    set_last_error("the product has too many tiles");
+    return QLORA_ERR_SHAPE;
+  }
+  auto kern = args.out_f32 ? k_fp4_gemm_pair<F, true> : k_fp4_gemm_pair<F, false>;
+  QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, num_sms() / 2));
+  QL_TRY(launch_pdl(kern, dim3(grid), dim3(kPairThreads), kPairSmem, st, tp, tq, sp, sq, xp, xq, to, args));
+  return QLORA_OK;
+}
+
+template <Fp4 F>
 qlora_status run_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
                          const Fp4Args& args, cudaStream_t st) {
   const int64_t M = a.rows;
+  if (M > 128) return run_pair<F>(a, b, ext, args, st);
   const int nt = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
   const int64_t tiles = static_cast<int64_t>(args.p_tiles) * ((M + nt - 1) / nt);
   int cs = 1;

@@ -553,25 +553,27 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
 constexpr int kLoraThreads = 192;  // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
 constexpr uint32_t kLoraABytes = 128 * kBK * 2;  // 16 KB
 // Pipeline depth: shared memory stays under 113 KB so that two CTAs share an SM.
-__host__ __device__ constexpr int lora_stages(int nc) { return nc == 128 ? 3 : 4; }
+__host__ __device__ constexpr int lora_stages(int nc) { return nc == 192 ? 2 : nc == 128 ? 3 : 4; }
+__host__ __device__ constexpr int lora_tmem(int nc) { return nc == 192 ? 256 : nc; }  // powers of two
 __host__ __device__ constexpr uint32_t lora_smem(int nc) {
   return lora_stages(nc) * (kLoraABytes + nc * kBK * 2) + 1024 + 256;
 }
 constexpr int kLoraCtasPerSm = 2;
-static_assert(lora_smem(128) <= 113 * 1024 && lora_smem(64) <= 113 * 1024, "two CTAs per SM");
+static_assert(lora_smem(192) <= 113 * 1024 && lora_smem(128) <= 113 * 1024 && lora_smem(64) <= 113 * 1024, "two CTAs per SM");
 
 struct LoraArgs {
   int steps_total;   // 64-wide contraction steps
   int steps_per;     // steps per split
   int tiles0;        // row tiles of the first problem; later tiles belong to the second
-  float* partial;    // [splits][rows_pad][64] fp32 (NC = 128: hi + lo columns summed)
+  float* partial;    // [splits][rows_pad][64] fp32 (NC > 64: the parts' columns summed)
   int64_t rows_pad;  // the problems' row tiles stacked: 128 x (tiles0 + tiles of the second)
   int* err;
 };
 
 // D[128-row tile, NC] = sum over this CTA's contraction range of A^T B (both bf16,
 // K-major or MN-major 128B-swizzled tiles loaded by TMA). With NC = 128 the B operand is
-// a bf16 hi | lo pair and the partial written is D[:, j] + D[:, 64 + j].
+// a bf16 hi | lo pair and the partial written is D[:, j] + D[:, 64 + j]; with NC = 192 it is
+// three bf16 parts, which hold an fp32 value to its last bit.
 // One launch may run two problems with the same contraction (operands tm_a/tm_b for
 // the first tiles0 row tiles, tm_a1/tm_b1 after); their partial rows are stacked.
 template <bool A_MN, bool B_MN, int NC>
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, NC);
+    tmem_alloc(tmem_slot, lora_tmem(NC));
     tmem_relinquish();
   }
   tc_fence_before();
@@ -702,9 +704,9 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
         if (have) {
           tmem_ld_32x32b_x32(taddr + c * 32, v);
           tmem_ld_wait();
-          if (NC == 128) {  // add the lo half of the pair
+          for (int part = 1; part < NC / 64; ++part) {  // add the lower parts
             uint32_t w[32];
-            tmem_ld_32x32b_x32(taddr + 64 + c * 32, w);
+            tmem_ld_32x32b_x32(taddr + part * 64 + c * 32, w);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -726,22 +728,34 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_d, NC);
+    tmem_dealloc(tmem_d, lora_tmem(NC));
   }
 }
 
 // ================================================================== finalize kernels
+// v as a sum of `parts` bf16 values, the largest first, at column j of each 64-wide part of
+// row m of out [M, 64 parts].
+__device__ __forceinline__ void store_parts(uint16_t* __restrict__ out, int64_t m, int j, float v,
+                                            int parts) {
+  for (int part = 0; part < parts; ++part) {
+    const uint16_t hi = bf16_bits_rn(v);
+    out[m * (64 * parts) + part * 64 + j] = hi;
+    v -= __uint_as_float(static_cast<uint32_t>(hi) << 16);
+  }
+}
+
 // T (or G) = sum of split partials [S][rows_pad][64]. Writes, where asked:
 //   plain fp32 [M, r]; bf16 hi/lo of scale * v [M, 128] (the K-extension operand);
-//   bf16 hi/lo of v [M, 128] (operand of the LoRA gradients).
-//   With t_in, also the bf16 hi/lo pair [M, 128] of that fp32 [M, r] (into t_hilo).
+//   v as `parts` bf16 parts [M, 64 parts] (operand of the LoRA gradients).
+//   With t_in, also the bf16 parts of that fp32 [M, r] (into t_hilo).
 //   With ga (one per row) and gb (one), scale * v is divided by both first: the operand of
 //   a product whose accumulator is multiplied by them at the end.
 __global__ void k_finalize_rank(const float* __restrict__ part, int splits, int64_t rows_pad,
                                 int64_t M, int r, float scale, float* __restrict__ plain,
                                 uint16_t* __restrict__ scaled, uint16_t* __restrict__ hilo,
                                 const float* __restrict__ t_in, uint16_t* __restrict__ t_hilo,
-                                const float* __restrict__ ga, const float* __restrict__ gb) {
+                                const float* __restrict__ ga, const float* __restrict__ gb,
+                                int parts) {
   griddep_wait_and_release();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= M * 64) return;
@@ -770,18 +784,8 @@ __global__ void k_finalize_rank(const float* __restrict__ part, int splits, int6
     scaled[m * 128 + j] = hi;
     scaled[m * 128 + 64 + j] = bf16_bits_rn(sv - __uint_as_float(static_cast<uint32_t>(hi) << 16));
   }
-  if (hilo) {
-    const uint16_t hi = bf16_bits_rn(v);
-    const float hv = __uint_as_float(static_cast<uint32_t>(hi) << 16);
-    hilo[m * 128 + j] = hi;
-    hilo[m * 128 + 64 + j] = bf16_bits_rn(v - hv);
-  }
-  if (t_hilo) {
-    const float tv = (j < r) ? t_in[m * r + j] : 0.f;
-    const uint16_t hi = bf16_bits_rn(tv);
-    t_hilo[m * 128 + j] = hi;
-    t_hilo[m * 128 + 64 + j] = bf16_bits_rn(tv - __uint_as_float(static_cast<uint32_t>(hi) << 16));
-  }
+  if (hilo) store_parts(hilo, m, j, v, parts);
+  if (t_hilo) store_parts(t_hilo, m, j, (j < r) ? t_in[m * r + j] : 0.f, parts);
 }
 
 // Both LoRA gradients from the stacked partials of one grouped launch:
@@ -990,7 +994,7 @@ qlora_status lora_down_T(const uint16_t* X, const uint16_t* A, const LinearShape
   const int64_t rows_pad = plan_split(s.M, s.K).rows_pad;
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                     splits, rows_pad, s.M, s.r, s.scale, t_plain, t_scaled, nullptr, nullptr,
-                    nullptr, ga, gb));
+                    nullptr, ga, gb, 2));
   return QLORA_OK;
 }
 
@@ -1100,7 +1104,7 @@ qlora_status gemm_backward(const uint16_t* dY, const uint16_t* X, const float* T
     QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
     QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                       splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, gs, ghl,
-                      t, thl, nullptr, nullptr));
+                      t, thl, nullptr, nullptr, 2));
   }
 
   // dX = dY W_hat + scale G A^T, and the grouped dA = scale X^T G (rows k) with
@@ -1180,7 +1184,7 @@ qlora_status gemm_shard_g(const uint16_t* dY, const uint16_t* B, const LinearSha
   QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                     splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, G_part, nullptr,
-                    nullptr, nullptr, nullptr, nullptr, nullptr));
+                    nullptr, nullptr, nullptr, nullptr, nullptr, 2));
   return QLORA_OK;
 }
 
@@ -1283,11 +1287,18 @@ size_t fp4_fwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matr
 }
 
 size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matrix* y, Fp4Out* yo,
-                      void** rest) {
+                      float** part, uint16_t** gs, uint16_t** g3, uint16_t** t3, float** t) {
   Carve c(ws);
   *y = carve_fp4(c, s.M, s.N, format, yo);
-  *rest = c.take<char>(0);
-  return c.off;
+  size_t pf = partial_floats(s.M, s.N, 64);                    // G = dY B^T
+  pf = std::max(pf, partial_floats(s.M, s.K, 64));             // T = X A (recompute)
+  pf = std::max(pf, partial_floats(stacked_rows(s.K, s.N), s.M, 192));  // dA and dB
+  *part = c.take<float>(pf);
+  *gs = c.take<uint16_t>(static_cast<size_t>(s.M) * 128);
+  *g3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
+  *t3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
+  *t = c.take<float>(static_cast<size_t>(s.M) * s.r);
+  return c.off + 256;
 }
 }  // namespace
 
@@ -1302,8 +1313,9 @@ size_t fp4_fwd_workspace(const LinearShape& s, int format) {
 size_t fp4_bwd_workspace(const LinearShape& s, int format) {
   qlora_fp4_matrix y;
   Fp4Out o;
-  void* rest;
-  return fp4_bwd_layout(s, format, nullptr, &y, &o, &rest) + gemm_bwd_workspace(s);
+  float *p, *t;
+  uint16_t *gs, *g3, *t3;
+  return fp4_bwd_layout(s, format, nullptr, &y, &o, &p, &gs, &g3, &t3, &t);
 }
 
 qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uint16_t* A,
@@ -1327,11 +1339,9 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
                           cudaStream_t st) {
   qlora_fp4_matrix y;
   Fp4Out yo;
-  void* rest;
-  fp4_bwd_layout(s, wt.format, ws, &y, &yo, &rest);
   float *part, *tbuf;
-  uint16_t *gs, *ghl, *thl;
-  bwd_layout(s, rest, &part, &gs, &ghl, &thl, &tbuf);
+  uint16_t *gs, *g3, *t3;
+  fp4_bwd_layout(s, wt.format, ws, &y, &yo, &part, &gs, &g3, &t3, &tbuf);
   const float* t = T_saved;
   if (!t) {
     qlora_status q = lora_down_T(X, A, s, part, tbuf, nullptr, st);
@@ -1345,12 +1355,12 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   QL_MAP(&tb, kBF16, B, s.N, s.r, s.N * 2, 64, 64, kSW128);    // B [r, N] K-major
   QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
-                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, gs, ghl, t,
-                    thl, dX ? y.gscale : nullptr, dX ? wt.gscale : nullptr));
+                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, gs, g3, t,
+                    t3, dX ? y.gscale : nullptr, dX ? wt.gscale : nullptr, 3));
   QL_MAP(&ga, kBF16, X, s.K, s.M, s.K * 2, 64, 64, kSW128);    // X as MN-major (k inner)
-  QL_MAP(&gb, kBF16, ghl, 128, s.M, 256, 64, 64, kSW128);      // G hi/lo MN-major
+  QL_MAP(&gb, kBF16, g3, 192, s.M, 384, 64, 64, kSW128);       // G in three parts, MN-major
   QL_MAP(&ga1, kBF16, dY, s.N, s.M, s.N * 2, 64, 64, kSW128);  // dY as MN-major (n inner)
-  QL_MAP(&gb1, kBF16, thl, 128, s.M, 256, 64, 64, kSW128);     // T hi/lo MN-major
+  QL_MAP(&gb1, kBF16, t3, 192, s.M, 384, 64, 64, kSW128);      // T in three parts, MN-major
   // dA and dB beside dX, as in gemm_backward
   SideStream* side = nullptr;
   if (dX) QL_TRY(side_stream(st, &side));
@@ -1367,7 +1377,7 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   }
   cudaError_t e = cudaSuccess;
   if (q == QLORA_OK)
-    e = run_lora_gemm<true, true, 128>(ga, gb, s.K, s.M, part, gst, &splits, &ga1, &gb1, s.N);
+    e = run_lora_gemm<true, true, 192>(ga, gb, s.K, s.M, part, gst, &splits, &ga1, &gb1, s.N);
   if (q == QLORA_OK && e == cudaSuccess) {
     const int64_t stacked = stacked_rows(s.K, s.N);
     e = launch_pdl(k_finalize_grad, dim3(blocks_for(stacked, kGradRows)), dim3(256), 0, gst, part,

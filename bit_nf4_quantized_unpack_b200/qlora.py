@@ -472,8 +472,19 @@ def qlora_adamw_step(p: torch.Tensor, g: torch.Tensor, state, step: int, *, lr: 
 
 
 # ------------------------------------------- microscaled 4-bit floating point (MXFP4, NVFP4)
+# A decode step makes several of these calls per linear, and at a few tokens the host is what
+# bounds them: the checks below read only cheap tensor attributes, and the raw stream handle
+# (0.1 us) takes the place of a Stream object (3.2 us).
 FP4_MXFP4, FP4_NVFP4 = 0, 1
 _FP4_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_U8, _BF, _FL = torch.uint8, torch.bfloat16, torch.float32
+_empty = torch.empty
+
+
+def _fp4_scales_bytes(rows: int, cols: int, fmt: int) -> int:
+    """qlora_fp4_scales_bytes without the call: tiles of 128 rows x 4 blocks of 512 bytes."""
+    per = 128 if fmt == FP4_MXFP4 else 64
+    return (rows + 127) // 128 * ((cols + per - 1) // per) * 512
 
 
 @dataclass
@@ -496,14 +507,12 @@ class FP4Matrix:
     def empty(rows: int, cols: int, fmt: int = FP4_NVFP4, device="cuda",
               gscale_rows: int | None = None) -> "FP4Matrix":
         """Uninitialised storage; gscale_rows: rows (default) or 1, NVFP4 only."""
-        nsc = int(lib().qlora_fp4_scales_bytes(rows, cols, fmt))
-        if rows and nsc == 0:
+        if rows < 0 or cols < 32 or cols % 32 or fmt not in (FP4_MXFP4, FP4_NVFP4):
             raise QLoraError(2, "FP4Matrix", f"[{rows}, {cols}], format {fmt}")
-        ng = rows if gscale_rows is None else gscale_rows
-        return FP4Matrix(torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
-                         torch.empty(nsc, dtype=torch.uint8, device=device),
-                         torch.empty(ng, dtype=torch.float32, device=device)
-                         if fmt == FP4_NVFP4 else None, rows, cols, fmt)
+        return FP4Matrix(_empty((rows, cols // 2), dtype=_U8, device=device),
+                         _empty(_fp4_scales_bytes(rows, cols, fmt), dtype=_U8, device=device),
+                         _empty(rows if gscale_rows is None else gscale_rows, dtype=_FL,
+                                device=device) if fmt == FP4_NVFP4 else None, rows, cols, fmt)
 
 
 @dataclass
@@ -513,122 +522,152 @@ class FP4Weight:
     wt: FP4Matrix | None = None
 
 
-def _fp4_tensor(t: torch.Tensor, name: str, dtypes, shape=None) -> torch.Tensor:
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+def _fp4_in(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
+    """The address of a dense CUDA tensor on device `dev` with this dtype and shape."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, "
+                         f"got {tuple(t.shape)} with strides {t.stride()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    return t.data_ptr()
 
 
-def _fp4_matrix(q: FP4Matrix, name: str) -> FP4Matrix:
-    """Checks that the buffers hold what the sizes say, so that no kernel reads past them."""
-    _fp4_tensor(q.codes, f"{name}.codes", (torch.uint8,))
-    _fp4_tensor(q.scales, f"{name}.scales", (torch.uint8,))
-    if q.codes.numel() != q.rows * (q.cols // 2):
-        raise ValueError(f"{name}.codes: {q.codes.numel()} bytes for [{q.rows}, {q.cols}]")
-    if q.scales.numel() != int(lib().qlora_fp4_scales_bytes(q.rows, q.cols, q.fmt)):
-        raise ValueError(f"{name}.scales: {q.scales.numel()} bytes for [{q.rows}, {q.cols}]")
-    if q.gscale is not None:
-        _fp4_tensor(q.gscale, f"{name}.gscale", (torch.float32,))
-        if q.gscale.numel() not in (1, q.rows):
-            raise ValueError(f"{name}.gscale: expected 1 or {q.rows} values")
-    return q
+def _fp4_device(t: torch.Tensor, name: str) -> int:
+    """The device index of the operand that the others have to share."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return t.get_device()
 
 
-def _fp4_device(*items):
-    """The one device of the operands, made current for the call (a kernel is launched on the
-    device and on the current stream of its operands)."""
-    devs = {t.device for t in items if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"operands on different devices: {sorted(map(str, devs))}")
-    return torch.cuda.device(devs.pop())
+def _fp4_matrix(q: FP4Matrix, name: str, dev: int) -> CFP4Matrix:
+    """The C form, after checking that the buffers hold what the sizes say (no kernel reads
+    past them)."""
+    rows, cols, g = q.rows, q.cols, q.gscale
+    return CFP4Matrix(
+        _fp4_in(q.codes, name + ".codes", dev, _U8, (rows, cols // 2)),
+        _fp4_in(q.scales, name + ".scales", dev, _U8, (_fp4_scales_bytes(rows, cols, q.fmt),)),
+        None if g is None else _fp4_in(g, name + ".gscale", dev, _FL, (rows,) if g.numel() != 1 else (1,)),
+        0 if g is None else g.numel(), rows, cols, q.fmt)
 
 
-def _workspace(workspace, need: int, device) -> torch.Tensor:
+def _fp4_workspace(workspace, need: int, dev: int, device):
+    """A byte buffer of at least `need` bytes (the library checks a caller's size)."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return _fp4_tensor(workspace, "workspace", (torch.uint8,))
+        return _empty(need if need > 16 else 16, dtype=_U8, device=device)
+    _fp4_in(workspace, "workspace", dev, _U8, workspace.shape)
+    return workspace
+
+
+def _fp4_call(name: str, dev: int, *args) -> None:
+    """One C call on the operands' device and its current stream."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        status = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status, name)
 
 
 def qlora_fp4_quantize(X: torch.Tensor, fmt: int = FP4_NVFP4,
                        out: FP4Matrix | None = None) -> FP4Matrix:
     """X [rows, cols] (fp32 or bf16, CUDA, contiguous) to microscaled form, each row by
     itself; cols % 32 == 0."""
-    _fp4_tensor(X, "X", _FP4_DTYPES)
+    lib()
+    dtype = _FP4_DTYPES.get(X.dtype)
+    if dtype is None:
+        raise TypeError(f"X: unsupported dtype {X.dtype}")
+    dev = _fp4_device(X, "X")
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     rows, cols = X.shape
-    q = out if out is not None else FP4Matrix.empty(rows, cols, fmt, X.device)
-    if (q.rows, q.cols, q.fmt) != (rows, cols, fmt):
+    x = _fp4_in(X, "X", dev, X.dtype, X.shape)
+    if out is None:
+        q = FP4Matrix.empty(rows, cols, fmt, X.device)
+        _fp4_call("qlora_fp4_quantize", dev, x, dtype, rows, cols, fmt, q.codes.data_ptr(),
+                  q.scales.data_ptr(), None if q.gscale is None else q.gscale.data_ptr())
+        return q
+    if (out.rows, out.cols, out.fmt) != (rows, cols, fmt):
         raise ValueError("out: another shape or format than X")
-    _fp4_matrix(q, "out")
-    if fmt == FP4_NVFP4 and (q.gscale is None or q.gscale.numel() != rows):
+    c = _fp4_matrix(out, "out", dev)
+    if fmt == FP4_NVFP4 and c.gscale_rows != rows:
         raise ValueError("out.gscale: expected one value per row")
-    with _fp4_device(X, q.codes, q.scales, q.gscale):
-        _check(lib().qlora_fp4_quantize(_ptr(X), _FP4_DTYPES[X.dtype], rows, cols, fmt,
-                                        _ptr(q.codes), _ptr(q.scales), _ptr(q.gscale), _stream()),
-               "qlora_fp4_quantize")
-    return q
+    _fp4_call("qlora_fp4_quantize", dev, x, dtype, rows, cols, fmt, c.codes, c.scales, c.gscale)
+    return out
 
 
 def qlora_fp4_quantize_weight(W: torch.Tensor, fmt: int = FP4_NVFP4, transposed: bool = True,
                               out: FP4Weight | None = None,
                               workspace: torch.Tensor | None = None) -> FP4Weight:
     """W [n_out, k_in] (fp32 or bf16, CUDA, contiguous, multiples of 32) with square blocks;
-    transposed: also the copy that the backward reads."""
-    _fp4_tensor(W, "W", _FP4_DTYPES)
+    transposed: also the copy that the backward reads (w and wt share one gscale)."""
+    lib()
+    dtype = _FP4_DTYPES.get(W.dtype)
+    if dtype is None:
+        raise TypeError(f"W: unsupported dtype {W.dtype}")
+    dev = _fp4_device(W, "W")
     if W.dim() != 2:
         raise ValueError("W must be 2-D")
     n, k = W.shape
+    src = _fp4_in(W, "W", dev, W.dtype, W.shape)
     if out is None:
-        w = FP4Matrix.empty(n, k, fmt, W.device, gscale_rows=1)
-        wt = FP4Matrix.empty(k, n, fmt, W.device, gscale_rows=1) if transposed else None
-        out = FP4Weight(w, wt)
-    w, wt = out.w, out.wt if transposed else None
-    if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
-            wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):
-        raise ValueError("out: another shape or format than W")
-    _fp4_matrix(w, "out.w")
+        w, wt = FP4Matrix.empty(n, k, fmt, W.device, gscale_rows=1), None
+        if transposed:
+            if n < 32 or n % 32:
+                raise QLoraError(2, "qlora_fp4_quantize_weight", f"[{n}, {k}]")
+            wt = FP4Matrix(_empty((k, n // 2), dtype=_U8, device=W.device),
+                           _empty(_fp4_scales_bytes(k, n, fmt), dtype=_U8, device=W.device),
+                           w.gscale, k, n, fmt)
+    else:
+        w, wt = out.w, out.wt if transposed else None
+        if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
+                wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):
+            raise ValueError("out: another shape or format than W")
+        if fmt == FP4_NVFP4 and (w.gscale is None or w.gscale.numel() != 1):
+            raise ValueError("out.w.gscale: expected one value")
+    c = _fp4_matrix(w, "out.w", dev)
+    tc = ts = None
     if wt is not None:
-        _fp4_matrix(wt, "out.wt")
-        wt.gscale = w.gscale  # one value for both
-    if fmt == FP4_NVFP4 and (w.gscale is None or w.gscale.numel() != 1):
-        raise ValueError("out.w.gscale: expected one value")
-    ws = _workspace(workspace, int(lib().qlora_fp4_quantize_weight_workspace_size()), W.device)
-    with _fp4_device(W, w.codes, w.scales, w.gscale, ws, *([wt.codes, wt.scales] if wt else [])):
-        _check(lib().qlora_fp4_quantize_weight(
-            _ptr(W), _FP4_DTYPES[W.dtype], n, k, fmt, _ptr(w.codes), _ptr(w.scales),
-            _ptr(w.gscale), _ptr(wt.codes if wt else None), _ptr(wt.scales if wt else None),
-            _ptr(ws), ws.numel(), _stream()), "qlora_fp4_quantize_weight")
+        wt.gscale = w.gscale
+        t = _fp4_matrix(wt, "out.wt", dev)
+        tc, ts = t.codes, t.scales
+    ws = _fp4_workspace(workspace, _lib.qlora_fp4_quantize_weight_workspace_size(), dev, W.device)
+    _fp4_call("qlora_fp4_quantize_weight", dev, src, dtype, n, k, fmt, c.codes, c.scales, c.gscale,
+              tc, ts, ws.data_ptr(), ws.numel())
     return FP4Weight(w, wt)
 
 
 def qlora_fp4_dequant(q: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
                       out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of a microscaled matrix [rows, cols], bf16 or fp32."""
-    _fp4_matrix(q, "q")
+    lib()
+    dev = _fp4_device(q.codes, "q.codes")
+    c = _fp4_matrix(q, "q", dev)
     if out is None:
-        out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
-    _fp4_tensor(out, "out", _FP4_DTYPES, (q.rows, q.cols))
-    with _fp4_device(q.codes, q.scales, q.gscale, out):
-        _check(lib().qlora_fp4_dequant(q.c_struct(), _FP4_DTYPES[out.dtype], _ptr(out), _stream()),
-               "qlora_fp4_dequant")
+        out = _empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
+    code = _FP4_DTYPES.get(out.dtype)
+    if code is None:
+        raise TypeError(f"out: unsupported dtype {out.dtype}")
+    o = _fp4_in(out, "out", dev, out.dtype, (q.rows, q.cols))
+    _fp4_call("qlora_fp4_dequant", dev, c, code, o)
     return out
 
 
 def qlora_fp4_matmul(a: FP4Matrix, b: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
                      out: torch.Tensor | None = None) -> torch.Tensor:
     """a b^T [a.rows, b.rows], bf16 or fp32; both operands of one format, b.rows % 8 == 0."""
-    _fp4_matrix(a, "a"), _fp4_matrix(b, "b")
+    lib()
+    dev = _fp4_device(a.codes, "a.codes")
+    ca, cb = _fp4_matrix(a, "a", dev), _fp4_matrix(b, "b", dev)
     if out is None:
-        out = torch.empty(a.rows, b.rows, dtype=dtype, device=a.codes.device)
-    _fp4_tensor(out, "out", _FP4_DTYPES, (a.rows, b.rows))
-    with _fp4_device(a.codes, a.scales, a.gscale, b.codes, b.scales, b.gscale, out):
-        _check(lib().qlora_fp4_matmul(a.c_struct(), b.c_struct(), _FP4_DTYPES[out.dtype],
-                                      _ptr(out), _stream()), "qlora_fp4_matmul")
+        out = _empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
+    code = _FP4_DTYPES.get(out.dtype)
+    if code is None:
+        raise TypeError(f"out: unsupported dtype {out.dtype}")
+    o = _fp4_in(out, "out", dev, out.dtype, (a.rows, b.rows))
+    _fp4_call("qlora_fp4_matmul", dev, ca, cb, code, o)
     return out
 
 
@@ -647,25 +686,23 @@ def qlora_fp4_linear_fwd(X: torch.Tensor, w: FP4Weight, A: torch.Tensor, B: torc
                          T: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Y = bf16(q(X) W^T + scale (X A) B) on a microscaled weight. Returns (Y, T) with
     T = X A (fp32) or None."""
-    q = _fp4_matrix(w.w, "w")
-    bf, dev = (torch.bfloat16,), X.device
-    M, r = X.shape[0], A.shape[1]
-    _fp4_tensor(X, "X", bf, (M, q.cols)), _fp4_tensor(A, "A", bf, (q.cols, r))
-    _fp4_tensor(B, "B", bf, (r, q.rows))
-    Y = Y if Y is not None else torch.empty(M, q.rows, dtype=torch.bfloat16, device=dev)
-    _fp4_tensor(Y, "Y", bf, (M, q.rows))
+    lib()
+    dev, q = _fp4_device(X, "X"), w.w
+    c = _fp4_matrix(q, "w", dev)
+    M, r, n, k, device = X.shape[0], A.shape[1], q.rows, q.cols, X.device
+    x, a = _fp4_in(X, "X", dev, _BF, (M, k)), _fp4_in(A, "A", dev, _BF, (k, r))
+    b = _fp4_in(B, "B", dev, _BF, (r, n))
+    if Y is None:
+        Y = _empty((M, n), dtype=_BF, device=device)
+    y, t = _fp4_in(Y, "Y", dev, _BF, (M, n)), None
     if save_T:
-        T = T if T is not None else torch.empty(M, r, dtype=torch.float32, device=dev)
-        _fp4_tensor(T, "T", (torch.float32,), (M, r))
-    else:
-        T = None
-    with _fp4_device(X, q.codes, q.scales, q.gscale, A, B, Y, T, workspace):
-        ws = _workspace(workspace, qlora_fp4_linear_fwd_workspace_size(M, q.rows, q.cols, r, q.fmt),
-                        dev)
-        _check(lib().qlora_fp4_linear_fwd(_ptr(X), M, q.c_struct(), _ptr(A), _ptr(B), r,
-                                          float(scale), _ptr(Y), _ptr(T), _ptr(ws), ws.numel(),
-                                          _stream()), "qlora_fp4_linear_fwd")
-    return Y, T
+        if T is None:
+            T = _empty((M, r), dtype=_FL, device=device)
+        t = _fp4_in(T, "T", dev, _FL, (M, r))
+    ws = _fp4_workspace(workspace, _lib.qlora_fp4_linear_fwd_workspace_size(M, n, k, r, q.fmt), dev,
+                        device)
+    _fp4_call("qlora_fp4_linear_fwd", dev, x, M, c, a, b, r, scale, y, t, ws.data_ptr(), ws.numel())
+    return Y, (T if save_T else None)
 
 
 def qlora_fp4_linear_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor | None, w: FP4Weight,
@@ -674,26 +711,28 @@ def qlora_fp4_linear_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor | No
                          dB: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Gradients (dX bf16 or None, dA fp32 [K, r], dB fp32 [r, N]) of qlora_fp4_linear_fwd;
     W is frozen and needs its transposed copy."""
-    if w.wt is None:
+    lib()
+    q = w.wt
+    if q is None:
         raise ValueError("w.wt: the backward reads the transposed copy")
-    q = _fp4_matrix(w.wt, "w.wt")
-    K, N, bf, f32, dev = q.rows, q.cols, (torch.bfloat16,), (torch.float32,), X.device
-    M, r = X.shape[0], A.shape[1]
-    _fp4_tensor(dY, "dY", bf, (M, N)), _fp4_tensor(X, "X", bf, (M, K))
-    _fp4_tensor(A, "A", bf, (K, r)), _fp4_tensor(B, "B", bf, (r, N))
-    if T is not None:
-        _fp4_tensor(T, "T", f32, (M, r))
+    dev = _fp4_device(X, "X")
+    c = _fp4_matrix(q, "w.wt", dev)
+    M, r, n, k, device = X.shape[0], A.shape[1], q.cols, q.rows, X.device
+    dy, x = _fp4_in(dY, "dY", dev, _BF, (M, n)), _fp4_in(X, "X", dev, _BF, (M, k))
+    a, b = _fp4_in(A, "A", dev, _BF, (k, r)), _fp4_in(B, "B", dev, _BF, (r, n))
+    t = None if T is None else _fp4_in(T, "T", dev, _FL, (M, r))
+    dx = None
     if need_dX:
-        dX = dX if dX is not None else torch.empty(M, K, dtype=torch.bfloat16, device=dev)
-        _fp4_tensor(dX, "dX", bf, (M, K))
-    else:
-        dX = None
-    dA = dA if dA is not None else torch.empty(K, r, dtype=torch.float32, device=dev)
-    dB = dB if dB is not None else torch.empty(r, N, dtype=torch.float32, device=dev)
-    _fp4_tensor(dA, "dA", f32, (K, r)), _fp4_tensor(dB, "dB", f32, (r, N))
-    with _fp4_device(dY, X, T, q.codes, q.scales, q.gscale, A, B, dX, dA, dB, workspace):
-        ws = _workspace(workspace, qlora_fp4_linear_bwd_workspace_size(M, N, K, r, q.fmt), dev)
-        _check(lib().qlora_fp4_linear_bwd(_ptr(dY), _ptr(X), _ptr(T), M, q.c_struct(), _ptr(A),
-                                          _ptr(B), r, float(scale), _ptr(dX), _ptr(dA), _ptr(dB),
-                                          _ptr(ws), ws.numel(), _stream()), "qlora_fp4_linear_bwd")
-    return dX, dA, dB
+        if dX is None:
+            dX = _empty((M, k), dtype=_BF, device=device)
+        dx = _fp4_in(dX, "dX", dev, _BF, (M, k))
+    if dA is None:
+        dA = _empty((k, r), dtype=_FL, device=device)
+    if dB is None:
+        dB = _empty((r, n), dtype=_FL, device=device)
+    da, db = _fp4_in(dA, "dA", dev, _FL, (k, r)), _fp4_in(dB, "dB", dev, _FL, (r, n))
+    ws = _fp4_workspace(workspace, _lib.qlora_fp4_linear_bwd_workspace_size(M, n, k, r, q.fmt), dev,
+                        device)
+    _fp4_call("qlora_fp4_linear_bwd", dev, dy, x, t, M, c, a, b, r, scale, dx, da, db,
+              ws.data_ptr(), ws.numel())
+    return (dX if need_dX else None), dA, dB
