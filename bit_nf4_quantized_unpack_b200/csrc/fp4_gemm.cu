@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   griddep_wait_and_release();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int issued = 0;
       const int64_t prow_tile = p0 / 128, qrow_tile = q0 / 128;
       const int nq = (NQ == 2 && args.Q - q0 > 128) ? 2 : 1;  // token scale tiles that exist
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
           mbar_wait_drain(&full[i % S], (i / S) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_ext = idesc_bf16_f32(kPRows, NT, args.ext_mn, false);
       bool ok = true;
       int done = 0;
@@ -374,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ TMA: this CTA's share of every step
-    if (lane == 0) {
+    if (elect_one()) {
       int n = 0;  // steps issued
       bool ok = true;
       for (int i = 0; i < my_tiles && ok; ++i) {
@@ -415,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc_ext = idesc_bf16_f32(kPairTile, kPairTile, args.ext_mn, false);
       const uint32_t ext_adv = args.ext_mn ? 128u : 2u;
       int n = 0;
@@ -524,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if constexpr (OUT_F32) {
           // the chunk fills both stage buffers: stage[token][row]
           const uint32_t st = smem_u32(stage2);
-          if (chunks >= 1 && lane == 0) bulk_wait_group_read<0>();
+          if (chunks >= 1 && elect_one()) bulk_wait_group_read<0>();
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -537,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           // token's 64 bytes are four 16-byte groups, group g at slot g ^ ((token >> 1) & 3),
           // the 64-byte swizzle of the tile store
           const uint32_t st = smem_u32(stage2) + (chunks & 1) * 2048;
-          if (chunks >= 2 && lane == 0) bulk_wait_group_read<1>();
+          if (chunks >= 2 && elect_one()) bulk_wait_group_read<1>();
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // tokens 8k..8k+7 of the chunk
@@ -559,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && p0 < args.P) {
+        if (p0 < args.P && elect_one()) {
           tma_store_2d(&tm_out, OUT_F32 ? stage2 : stage2 + (chunks & 1) * 2048, static_cast<int>(p0),
                        static_cast<int>(q));
           bulk_commit_group();
@@ -586,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tmem_ld_wait();
       emit(3, v1);
     }
-    if (lane == 0) bulk_wait_group_all();  // tile stores done before the CTA exits
+    if (elect_one()) bulk_wait_group_all();  // tile stores done before the CTA exits
   }
   // The MMAs are complete and the arrivals of the last commits have landed, in each CTA, before
   // tensor memory and the barriers go.
