@@ -7,7 +7,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 256;  // tile coordinates are 32-bit
 constexpr int64_t kMaxValues = int64_t{1} << 40;        // grid dimensions of the codec kernels
-constexpr int64_t kMaxWeightRows = (int64_t{1} << 22) - 64;
+constexpr int64_t kMaxWeightRows = int64_t{65535} * 32;  // the weight kernel's grid
 constexpr size_t kWeightWorkspace = 256;
 
 bool known_format(int32_t f) { return f == QLORA_FP4_MX || f == QLORA_FP4_NV; }

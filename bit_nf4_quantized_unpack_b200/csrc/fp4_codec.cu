@@ -23,86 +23,134 @@ namespace qlora {
 namespace {
 
 constexpr int kChunk = 16;  // values per thread and step: 32 bytes of bf16, 64 of fp32
-
-struct Raw16Bf { uint4 a, b; };
-struct Raw16F { float4 a, b, c, d; };
-template <bool BF16> struct RawOf { using T = Raw16Bf; };
-template <> struct RawOf<false> { using T = Raw16F; };
-
-template <bool BF16>
-__device__ __forceinline__ typename RawOf<BF16>::T load16(const void* base, int64_t elem) {
-  typename RawOf<BF16>::T r;
-  if constexpr (BF16) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
-    r.a = __ldg(p);
-    r.b = __ldg(p + 1);
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
-    r.a = __ldg(p);
-    r.b = __ldg(p + 1);
-    r.c = __ldg(p + 2);
-    r.d = __ldg(p + 3);
-  }
-  return r;
-}
-__device__ __forceinline__ void expand2(uint32_t w, float* v) {
-  v[0] = __uint_as_float(w << 16);
-  v[1] = __uint_as_float(w & 0xFFFF0000u);
-}
-__device__ __forceinline__ void expand(const Raw16Bf& r, float (&v)[16]) {
-  expand2(r.a.x, v), expand2(r.a.y, v + 2), expand2(r.a.z, v + 4), expand2(r.a.w, v + 6);
-  expand2(r.b.x, v + 8), expand2(r.b.y, v + 10), expand2(r.b.z, v + 12), expand2(r.b.w, v + 14);
-}
-__device__ __forceinline__ void expand(const Raw16F& r, float (&v)[16]) {
-  v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w;
-  v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
-  v[8] = r.c.x, v[9] = r.c.y, v[10] = r.c.z, v[11] = r.c.w;
-  v[12] = r.d.x, v[13] = r.d.y, v[14] = r.d.z, v[15] = r.d.w;
-}
-
-// Largest finite magnitude (fp32 bits) of 16 values; bit 31 is set when one is not finite.
-__device__ __forceinline__ uint32_t amax16(const float (&v)[16]) {
-  uint32_t m = 0u;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, finite_mag(v[i], bad));
-  return bad ? m | 0x80000000u : m;
-}
 constexpr uint32_t kMag = 0x7FFFFFFFu;
-// Combines two amax16 results.
-__device__ __forceinline__ uint32_t amax_join(uint32_t a, uint32_t b) {
-  return max(a & kMag, b & kMag) | ((a | b) & 0x80000000u);
+constexpr uint32_t kInf = 0x7F800000u;
+
+// 16 values as loaded, and their largest magnitude as fp32 bits (kInf or above when one of
+// them is not finite: magnitudes order like unsigned integers, NaNs last).
+template <bool BF16>
+struct Raw16;
+template <>
+struct Raw16<true> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const void* base, int64_t elem) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
+    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi = max(hi, w[i] & kMag);          // the odd value, and bits below it that cannot raise
+      lo = max(lo, w[i] << 16 & kMag);    // it past the next bf16
+    }
+    return max(hi & 0xFFFF0000u, lo);
+  }
+};
+template <>
+struct Raw16<false> {
+  float v[16];
+  __device__ __forceinline__ void load(const void* base, int64_t elem) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 q = __ldg(p + i);
+      v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  }
+  __device__ __forceinline__ float at(int i) const { return v[i]; }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & kMag);
+    return m;
+  }
+};
+
+// The largest finite magnitude, for the rare block whose amax() is not finite.
+template <typename R>
+__device__ __forceinline__ uint32_t finite_amax(const R& r) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = __float_as_uint(r.at(i)) & kMag;
+    if (b < kInf) m = max(m, b);
+  }
+  return m;
 }
 
-// Scale byte of a block from its amax16; g_inv = 1 / gscale (NVFP4).
+// x / d for positive normal d, correctly rounded: the reciprocal's product and one correction
+// by its exact remainder. (Results below the normal range only round to the code 0.)
+__device__ __forceinline__ float div_rn(float x, float d, float rcp) {
+  const float q = x * rcp;
+  return __fmaf_rn(__fmaf_rn(-q, d, x), rcp, q);
+}
+
+// Scale byte of a block from its largest magnitude; g_inv = 1 / gscale (NVFP4).
 template <Fp4 F>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t am, float g_inv) {
-  if (am & 0x80000000u) return kFp4NanScale<F>;
+  if (am >= kInf) return kFp4NanScale<F>;
   if (F == Fp4::kMx) {
     const int biased = static_cast<int>(am >> 23) - 2;  // floor(log2) - 2 + 127
     return static_cast<uint32_t>(max(biased, 0));       // zero and subnormal maxima: 2^-127
   }
-  return e4m3_bits(__fdiv_rn(__uint_as_float(am) * g_inv, 6.f));
+  return e4m3_bits(div_rn(__uint_as_float(am) * g_inv, 6.f, 1.f / 6.f));
 }
 
-// Codes of 16 values under one scale byte (low nibble first).
+// What turns a value into the argument of e2m1() under one scale byte.
 template <Fp4 F>
-__device__ __forceinline__ uint2 codes16(const float (&v)[16], uint32_t sb, float g_inv) {
-  if (sb == kFp4NanScale<F> || (F == Fp4::kNv && sb == 0u)) return make_uint2(0u, 0u);
-  float y[16];
-  if (F == Fp4::kMx) {
-    const float inv = pow2_f32(127 - static_cast<int>(sb));
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = v[i] * inv;
-  } else {
-    const float c = fp4_scale_value<F>(sb);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(v[i] * g_inv, c);
+struct Encoder {
+  float mul, div, rcp;  // MX: x * mul; NV: x * mul / div, mul = 0 for codes that are all 0
+  __device__ __forceinline__ Encoder(uint32_t sb, float g_inv) {
+    if (F == Fp4::kMx) {
+      mul = sb == kFp4NanScale<F> ? 0.f : pow2_f32(127 - static_cast<int>(sb));
+    } else {
+      const bool none = sb == 0u || sb == kFp4NanScale<F>;
+      mul = none ? 0.f : g_inv;
+      div = none ? 1.f : fp4_scale_value<F>(sb);
+      rcp = __frcp_rn(div);
+    }
   }
-  float lo[8], hi[8];
+  __device__ __forceinline__ bool zero() const { return mul == 0.f; }
+  // eight values, v(i), to eight codes
+  template <typename V>
+  __device__ __forceinline__ uint32_t encode8(V&& v) const {
+    float y[8];
+    if (F == Fp4::kMx) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) lo[i] = y[i], hi[i] = y[8 + i];
-  return make_uint2(fp4_pack8(lo), fp4_pack8(hi));
+      for (int i = 0; i < 8; ++i) y[i] = v(i) * mul;
+    } else {
+      const uint64_t m2 = f2_pack(mul, mul), r2 = f2_pack(rcp, rcp), d2 = f2_pack(-div, -div);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {  // div_rn on pairs
+        const uint64_t x = f2_mul(f2_pack(v(i), v(i + 1)), m2);
+        const uint64_t q = f2_mul(x, r2);
+        f2_unpack(f2_fma(f2_fma(q, d2, x), r2, q), y[i], y[i + 1]);
+      }
+    }
+    return fp4_pack8(y);
+  }
+};
+
+// Codes of 16 values under one scale byte (low nibble first).
+template <Fp4 F, typename R>
+__device__ __forceinline__ uint2 codes16(const R& r, uint32_t sb, float g_inv) {
+  const Encoder<F> e(sb, g_inv);
+  if (e.zero()) return make_uint2(0u, 0u);
+  return make_uint2(e.encode8([&](int i) { return r.at(i); }),
+                    e.encode8([&](int i) { return r.at(8 + i); }));
 }
 
 // The scale bytes of four consecutive blocks as one word, valid in the lane that holds the
@@ -116,65 +164,64 @@ __device__ __forceinline__ uint32_t gather4(uint32_t sb) {
 }
 
 // ------------------------------------------------------------------ MXFP4 rows
-// A warp takes 512 columns of one row, 16 per lane.
+// A warp takes 512 columns of one row, 16 per lane; neighbouring warps take neighbouring rows,
+// whose scale bytes share sectors.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    k_fp4_quantize_mx(const void* __restrict__ X, int64_t rows, int64_t cols, int segs,
+    k_fp4_quantize_mx(const void* __restrict__ X, uint32_t rows, int64_t cols,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   griddep_wait_and_release();
   const int lane = threadIdx.x & 31;
-  const int64_t task = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t row = task / segs;
+  const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const int64_t col = (task - row * segs) * 512 + lane * kChunk;
-  const bool in = col < cols;
-  float v[16] = {};
-  if (in) expand(load16<BF16>(X, row * cols + col), v);
-  uint32_t am = amax16(v);
-  am = amax_join(am, __shfl_xor_sync(~0u, am, 1));
-  const uint32_t sb = in ? scale_byte<Fp4::kMx>(am, 1.f) : 0u;
-  if (in)
-    *reinterpret_cast<uint2*>(codes + (row * cols + col) / 2) = codes16<Fp4::kMx>(v, sb, 1.f);
-  const uint32_t w = gather4<Fp4::kMx>(sb);
-  if ((lane & 7) == 0 && in)
-    *reinterpret_cast<uint32_t*>(
-        scales + fp4_scale_offset(row, col / 32, (cols + 127) / 128)) = w;
+  for (int64_t seg = blockIdx.y; seg * 512 < cols; seg += gridDim.y) {
+    const int64_t col = seg * 512 + lane * kChunk;
+    const bool in = col < cols;
+    Raw16<BF16> r;
+    if (in) r.load(X, row * cols + col);
+    else r.zero();
+    uint32_t am = r.amax();
+    am = max(am, __shfl_xor_sync(~0u, am, 1));
+    const uint32_t sb = in ? scale_byte<Fp4::kMx>(am, 1.f) : 0u;
+    if (in)
+      *reinterpret_cast<uint2*>(codes + (row * cols + col) / 2) = codes16<Fp4::kMx>(r, sb, 1.f);
+    const uint32_t w = gather4<Fp4::kMx>(sb);
+    if ((lane & 7) == 0 && in)
+      *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, col / 32, (cols + 127) / 128)) = w;
+  }
 }
 
 // ------------------------------------------------------------------ NVFP4 rows
 // One CTA per row; the row stays in registers (U chunks a thread) between the row maximum
 // and the codes. U = 0: rows too long for that are read twice.
 template <bool BF16, int U>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
     k_fp4_quantize_nv(const void* __restrict__ X, int64_t cols, uint8_t* __restrict__ codes,
                       uint8_t* __restrict__ scales, float* __restrict__ gscale) {
   griddep_wait_and_release();
-  __shared__ uint32_t part[8];
+  __shared__ uint32_t part[16];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int64_t row = blockIdx.x;
-  const int64_t chunks = cols / kChunk, padded = (chunks + 3) & ~int64_t{3};
-  typename RawOf<BF16>::T raw[U > 0 ? U : 1];
+  const int chunks = static_cast<int>(cols / kChunk), padded = (chunks + 3) & ~3;
+  Raw16<BF16> raw[U > 0 ? U : 1];
   uint32_t top = 0u;
+  auto join = [&](const Raw16<BF16>& r) {
+    uint32_t m = r.amax();
+    if (m >= kInf) m = finite_amax(r);
+    top = max(top, m);
+  };
   if constexpr (U > 0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t c = tid + static_cast<int64_t>(u) * nt;
-      if (c < chunks) raw[u] = load16<BF16>(X, row * cols + c * kChunk);
+      if (tid + u * nt < chunks) raw[u].load(X, row * cols + static_cast<int64_t>(tid + u * nt) * kChunk);
+      else raw[u].zero();
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = tid + static_cast<int64_t>(u) * nt;
-      if (c < chunks) {
-        float v[16];
-        expand(raw[u], v);
-        top = max(top, amax16(v) & kMag);
-      }
-    }
+    for (int u = 0; u < U; ++u) join(raw[u]);
   } else {
-    for (int64_t c = tid; c < chunks; c += nt) {
-      float v[16];
-      expand(load16<BF16>(X, row * cols + c * kChunk), v);
-      top = max(top, amax16(v) & kMag);
+    for (int c = tid; c < chunks; c += nt) {
+      raw[0].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
+      join(raw[0]);
     }
   }
   top = __reduce_max_sync(~0u, top);
@@ -185,29 +232,25 @@ __global__ void __launch_bounds__(256)
   if (tid == 0) gscale[row] = pow2_f32(e);
   const float g_inv = pow2_f32(-e);
   const int64_t ktiles = padded / 4;
-  auto emit = [&](int64_t c, const float (&v)[16], bool in) {
-    const uint32_t sb = in ? scale_byte<Fp4::kNv>(amax16(v), g_inv) : 0u;
+  auto emit = [&](int c, const Raw16<BF16>& r) {
+    const bool in = c < chunks;
+    const uint32_t sb = in ? scale_byte<Fp4::kNv>(r.amax(), g_inv) : 0u;
     if (in)
-      *reinterpret_cast<uint2*>(codes + (row * cols + c * kChunk) / 2) =
-          codes16<Fp4::kNv>(v, sb, g_inv);
+      *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<int64_t>(c) * (kChunk / 2)) =
+          codes16<Fp4::kNv>(r, sb, g_inv);
     const uint32_t w = gather4<Fp4::kNv>(sb);
     if ((c & 3) == 0 && c < padded)
       *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, c, ktiles)) = w;
   };
   if constexpr (U > 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = tid + static_cast<int64_t>(u) * nt;
-      if (c - tid >= padded) break;  // the same in every thread
-      float v[16] = {};
-      if (c < chunks) expand(raw[u], v);
-      emit(c, v, c < chunks);
-    }
+    for (int u = 0; u < U; ++u)
+      if (u * nt < padded) emit(tid + u * nt, raw[u]);
   } else {
-    for (int64_t c = tid; c - tid < padded; c += nt) {
-      float v[16] = {};
-      if (c < chunks) expand(load16<BF16>(X, row * cols + c * kChunk), v);
-      emit(c, v, c < chunks);
+    for (int c = tid; c - tid < padded; c += nt) {
+      if (c < chunks) raw[0].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
+      else raw[0].zero();
+      emit(c, raw[0]);
     }
   }
 }
@@ -218,21 +261,48 @@ template <bool BF16>
 __global__ void __launch_bounds__(256)
     k_fp4_amax(const void* __restrict__ W, int64_t chunks, uint32_t* __restrict__ top) {
   griddep_wait_and_release();
+  constexpr int U = BF16 ? 4 : 2;  // chunks in flight per thread
   uint32_t m = 0u;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; c < chunks;
-       c += stride) {
-    float v[16];
-    expand(load16<BF16>(W, c * kChunk), v);
-    m = max(m, amax16(v) & kMag);
+       c += stride * U) {
+    Raw16<BF16> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c + u * stride < chunks) r[u].load(W, (c + u * stride) * kChunk);
+      else r[u].zero();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t a = r[u].amax();
+      if (a >= kInf) a = finite_amax(r[u]);
+      m = max(m, a);
+    }
   }
   m = __reduce_max_sync(~0u, m);
   if ((threadIdx.x & 31) == 0 && m) atomicMax(top, m);  // a maximum: no order to depend on
 }
 
-// A 64 x 64 tile of W: block scales from the maxima of b x b squares, codes written once
-// along the rows and, through shared memory, once along the columns (the transposed copy
-// has the same squares, so it stores the same values).
+// Transpose of an 8 x 8 square of nibbles, one word per row: swaps 4 x 4, 2 x 2 and single
+// nibbles across the diagonal.
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int s = 4; s >= 1; s >>= 1) {
+    const uint32_t mask = s == 4 ? 0x0000FFFFu : s == 2 ? 0x00FF00FFu : 0x0F0F0F0Fu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & s) continue;
+      const uint32_t t = (w[i] >> (4 * s) ^ w[i + s]) & mask;
+      w[i + s] ^= t;
+      w[i] ^= t << (4 * s);
+    }
+  }
+}
+
+// A warp takes 32 rows x 64 columns of W, a lane 8 x 8 of it (lane = row group * 8 + column
+// group), so that squares of 16 and of 32 are whole in the warp: the maxima go through
+// shuffles, the transposed codes through an 8 x 8 nibble transpose in registers. The
+// transposed copy has the same squares, so it stores the same values.
 template <Fp4 F, bool BF16>
 __global__ void __launch_bounds__(256)
     k_fp4_quantize_weight(const void* __restrict__ W, int64_t n, int64_t k,
@@ -241,141 +311,182 @@ __global__ void __launch_bounds__(256)
                           uint8_t* __restrict__ t_codes, uint8_t* __restrict__ t_scales) {
   griddep_wait_and_release();
   constexpr int B = kFp4Block<F>;
-  constexpr int NB = 64 / B;               // blocks along a side of the tile
-  __shared__ uint32_t part[8][4];          // maxima of 8 rows x 16 columns
-  __shared__ uint8_t sbs[4][4];            // scale bytes of the tile's squares
-  __shared__ uint8_t tile[64][64 + 4];     // codes, one per byte: [row][column]
-  const int tid = threadIdx.x, row = tid >> 2, seg = tid & 3;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 64, k0 = static_cast<int64_t>(blockIdx.x) * 64;
+  const int lane = threadIdx.x & 31, kl = lane & 7, nl = lane >> 3;
+  const int64_t k0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 64;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 32;
+  if (k0 >= k) return;
   float g_inv = 1.f;
   if (F == Fp4::kNv) {
-    const int e = nv_gscale_exp(*top);
+    const int e = nv_gscale_exp(__ldg(top));
     g_inv = pow2_f32(-e);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *gscale = pow2_f32(e);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *gscale = pow2_f32(e);
   }
-  const int64_t gn = n0 + row, gk = k0 + seg * 16;
-  const bool in = gn < n && gk < k;
-  float v[16] = {};
-  if (in) expand(load16<BF16>(W, gn * k + gk), v);
-  uint32_t am = amax16(v);
-  am = amax_join(am, __shfl_xor_sync(~0u, am, 4));
-  am = amax_join(am, __shfl_xor_sync(~0u, am, 8));
-  am = amax_join(am, __shfl_xor_sync(~0u, am, 16));
-  if ((tid & 31) < 4) part[tid >> 5][seg] = am;
-  __syncthreads();
-  if (tid < NB * NB) {
-    const int br = tid / NB, bc = tid % NB;
-    uint32_t m = 0u;
-    for (int i = 0; i < B / 8; ++i)
-      for (int j = 0; j < B / 16; ++j) m = amax_join(m, part[br * (B / 8) + i][bc * (B / 16) + j]);
-    sbs[br][bc] = static_cast<uint8_t>(scale_byte<F>(m, g_inv));
-  }
-  __syncthreads();
-  const uint2 q = codes16<F>(v, sbs[row / B][seg * 16 / B], g_inv);
-  if (in) *reinterpret_cast<uint2*>(codes + (gn * k + gk) / 2) = q;
+  const int64_t gk = k0 + kl * 8, gn = n0 + nl * 8;
+  const bool in = gk < k;  // n is a multiple of 32, k of 32
+  // rows of eight values
+  uint4 rb[BF16 ? 8 : 1];
+  float4 rf[BF16 ? 1 : 16];
+  uint32_t am = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // word of four codes, one per byte
-    const uint32_t w16 = ((i & 2) ? q.y : q.x) >> ((i & 1) * 16);
-    *reinterpret_cast<uint32_t*>(&tile[row][seg * 16 + i * 4]) =
-        (w16 & 0xFu) | (w16 & 0xF0u) << 4 | (w16 & 0xF00u) << 8 | (w16 & 0xF000u) << 12;
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (BF16) {
+      rb[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (in) rb[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + (gn + i) * k + gk));
+    } else {
+      rf[2 * i] = rf[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (in) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(W) + (gn + i) * k + gk);
+        rf[2 * i] = __ldg(p);
+        rf[2 * i + 1] = __ldg(p + 1);
+      }
+    }
   }
-  // scale bytes: NB per row of the tile and, transposed, NB per column. Blocks of 16: the
-  // tile is one scale tile wide (four blocks); blocks of 32: half of one. Blocks past the
-  // edge of W but inside its last scale tile are written as zeros.
-  if (tid < 64) {
-    const int64_t ktiles = (k / B + 3) / 4;
-    if (n0 + tid < n) {
-      for (int b = 0; b < NB; ++b) {
-        const int64_t blk = k0 / B + b;
-        if (blk < ktiles * 4)
-          scales[fp4_scale_offset(n0 + tid, blk, ktiles)] = blk * B < k ? sbs[tid / B][b] : 0;
-      }
-      if (F == Fp4::kMx && k0 + 64 >= k)  // the rest of the last tile's four blocks
-        for (int64_t blk = k0 / B + NB; blk < ktiles * 4; ++blk)
-          scales[fp4_scale_offset(n0 + tid, blk, ktiles)] = 0;
+  auto at = [&](int i, int j) -> float {
+    if constexpr (BF16) {
+      const uint32_t w = j < 2 ? rb[i].x : j < 4 ? rb[i].y : j < 6 ? rb[i].z : rb[i].w;
+      return __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
+    } else {
+      const float4 q = rf[2 * i + (j >> 2)];
+      return (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
     }
-  } else if (tid < 128 && t_codes) {
-    const int c = tid - 64;
-    const int64_t ktiles = (n / B + 3) / 4;
-    if (k0 + c < k) {
-      for (int b = 0; b < NB; ++b) {
-        const int64_t blk = n0 / B + b;
-        if (blk < ktiles * 4)
-          t_scales[fp4_scale_offset(k0 + c, blk, ktiles)] = blk * B < n ? sbs[b][c / B] : 0;
-      }
-      if (F == Fp4::kMx && n0 + 64 >= n)
-        for (int64_t blk = n0 / B + NB; blk < ktiles * 4; ++blk)
-          t_scales[fp4_scale_offset(k0 + c, blk, ktiles)] = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(at(i, j)) & kMag);
+  am = max(am, __shfl_xor_sync(~0u, am, 1));
+  am = max(am, __shfl_xor_sync(~0u, am, 8));
+  if (F == Fp4::kMx) {
+    am = max(am, __shfl_xor_sync(~0u, am, 2));
+    am = max(am, __shfl_xor_sync(~0u, am, 16));
+  }
+  const uint32_t sb = in ? scale_byte<F>(am, g_inv) : 0u;
+  const Encoder<F> enc(sb, g_inv);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = enc.encode8([&](int j) { return at(i, j); });
+    if (enc.zero()) w[i] = 0u;
+    if (in) *reinterpret_cast<uint32_t*>(codes + ((gn + i) * k + gk) / 2) = w[i];
+  }
+  if (t_codes) {
+    transpose_nibbles(w);
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint32_t*>(t_codes + ((gk + j) * n + gn) / 2) = w[j];
     }
+  }
+  // Scale bytes. Lane l writes row l of W (64 / B blocks) and rows l, l + 32 of the transpose
+  // (32 / B blocks). Blocks past the edge but inside the last scale tile are 0: lanes outside
+  // have sb = 0, and the warp at the edge fills up what no warp covers.
+  const int64_t kt = (k / B + 3) / 4, tt = (n / B + 3) / 4;
+  const int src = (lane >> 3) * 8;  // the lane that holds (row lane, column group 0)
+  if (F == Fp4::kNv) {
+    uint32_t v = 0u;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) v |= __shfl_sync(~0u, sb, src + 2 * b) << (8 * b);
+    *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(n0 + lane, k0 / 16, kt)) = v;
+  } else {
+    const uint32_t v = __shfl_sync(~0u, sb, src) | __shfl_sync(~0u, sb, src + 4) << 8;
+    *reinterpret_cast<uint16_t*>(scales + fp4_scale_offset(n0 + lane, k0 / 32, kt)) = static_cast<uint16_t>(v);
+    if (k0 + 64 >= k && (k0 / 32) % 4 == 0)
+      *reinterpret_cast<uint16_t*>(scales + fp4_scale_offset(n0 + lane, k0 / 32 + 2, kt)) = 0;
   }
   if (!t_codes) return;
-  __syncthreads();
-  // column c of the tile, 16 rows from r0: eight bytes of the transposed codes
-  const int c = tid >> 2, r0 = (tid & 3) * 16;
-  if (k0 + c < k && n0 + r0 < n) {
-    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i >> 3] |= static_cast<uint32_t>(tile[r0 + i][c]) << (4 * (i & 7));
-    *reinterpret_cast<uint2*>(t_codes + ((k0 + c) * n + n0 + r0) / 2) = make_uint2(w[0], w[1]);
+  for (int h = 0; h < 2; ++h) {
+    const int row = lane + 32 * h, from = row >> 3;  // column group of W's lane 0..7
+    if (F == Fp4::kNv) {
+      const uint32_t v = __shfl_sync(~0u, sb, from) | __shfl_sync(~0u, sb, from + 16) << 8;
+      if (k0 + row < k) {
+        *reinterpret_cast<uint16_t*>(t_scales + fp4_scale_offset(k0 + row, n0 / 16, tt)) = static_cast<uint16_t>(v);
+        if (n0 + 32 >= n && (n0 / 16) % 4 == 0)
+          *reinterpret_cast<uint16_t*>(t_scales + fp4_scale_offset(k0 + row, n0 / 16 + 2, tt)) = 0;
+      }
+    } else {
+      const uint32_t v = __shfl_sync(~0u, sb, from);
+      if (k0 + row < k) {
+        t_scales[fp4_scale_offset(k0 + row, n0 / 32, tt)] = static_cast<uint8_t>(v);
+        if (n0 + 32 >= n)
+          for (int64_t b = n0 / 32 + 1; b < tt * 4; ++b) t_scales[fp4_scale_offset(k0 + row, b, tt)] = 0;
+      }
+    }
   }
 }
 
 // ------------------------------------------------------------------ reading back
-// A lane takes eight columns of one row. value = fl32(fl32(code * scale) * gscale); the first
-// product is exact (1 + 3 mantissa bits), then one rounding to bf16 where asked.
+// A warp takes 1024 columns of one row in strides of 32 lanes; a lane's share of a stride is
+// 16 bytes of output. Neighbouring warps take neighbouring rows, whose scale bytes share
+// sectors. value = fl32(fl32(code * scale) * gscale); the first product is exact (1 + 3
+// mantissa bits), then one rounding to bf16 where asked.
 template <Fp4 F, bool BF16>
 __global__ void __launch_bounds__(256)
     k_fp4_dequant(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                  const float* __restrict__ gscale, bool g_per_row, int64_t rows, int64_t cols,
+                  const float* __restrict__ gscale, bool g_per_row, uint32_t rows, int64_t cols,
                   int64_t ktiles, void* __restrict__ out) {
   griddep_wait_and_release();
-  const int64_t per_row = cols / 8, total = rows * per_row;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += stride) {
-    const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    const float s = fp4_scale_value<F>(__ldg(scales + fp4_scale_offset(row, col / kFp4Block<F>, ktiles)));
-    const float g = gscale ? __ldg(gscale + (g_per_row ? row : 0)) : 1.f;
-    uint32_t h[4];
-    fp4_unpack8(w, h);
-    float v[8];
+  constexpr int V = BF16 ? 8 : 4;          // values per lane and stride
+  constexpr int U = 1024 / (32 * V);       // strides
+  const int lane = threadIdx.x & 31;
+  const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const float g = gscale ? __ldg(gscale + (g_per_row ? row : 0)) : 1.f;
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * 1024; c0 < cols; c0 += static_cast<int64_t>(gridDim.y) * 1024) {
+    uint32_t w[U], sb[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\t"
-          "cvt.f32.f16 %1, hi;\n\t}"
-          : "=f"(v[2 * j]), "=f"(v[2 * j + 1])
-          : "r"(h[j]));
-      v[2 * j] = v[2 * j] * s * g;
-      v[2 * j + 1] = v[2 * j + 1] * s * g;
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = c0 + (u * 32 + lane) * V;
+      w[u] = sb[u] = 0u;
+      if (col < cols) {
+        const uint8_t* src = codes + (row * cols + col) / 2;
+        w[u] = BF16 ? __ldg(reinterpret_cast<const uint32_t*>(src))
+                    : __ldg(reinterpret_cast<const uint16_t*>(src));
+        sb[u] = __ldg(scales + fp4_scale_offset(row, col / kFp4Block<F>, ktiles));
+      }
     }
-    if (BF16) {
-      reinterpret_cast<uint4*>(out)[i] =
-          make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
-                     pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
-    } else {
-      reinterpret_cast<float4*>(out)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(out)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t col = c0 + (u * 32 + lane) * V;
+      if (col >= cols) break;
+      const float s = fp4_scale_value<F>(sb[u]);
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 f = e2m1_pair(w[u] >> (8 * j));
+        v[2 * j] = f.x * s * g;
+        v[2 * j + 1] = f.y * s * g;
+      }
+      if constexpr (BF16)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * cols + col) =
+            make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                       pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + row * cols + col) =
+            make_float4(v[0], v[1], v[2], v[3]);
     }
   }
 }
+
+constexpr int64_t kMaxGridY = 65535;
 
 template <bool BF16>
 cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format, uint8_t* codes,
                           uint8_t* scales, float* gscale, cudaStream_t st) {
   if (format == QLORA_FP4_MX) {
-    const int segs = static_cast<int>((cols + 511) / 512);
-    const int64_t blocks = (rows * segs + 7) / 8;
-    return launch_pdl(k_fp4_quantize_mx<BF16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                      st, X, rows, cols, segs, codes, scales);
+    const dim3 grid(static_cast<unsigned>((rows + 7) / 8),
+                    static_cast<unsigned>(std::min((cols + 511) / 512, kMaxGridY)));
+    return launch_pdl(k_fp4_quantize_mx<BF16>, grid, dim3(256), 0, st, X,
+                      static_cast<uint32_t>(rows), cols, codes, scales);
   }
+  // chunks a thread: as few as 512 threads (256 where one is enough) allow, while the row
+  // fits the registers (32 a chunk of bf16 with its temporaries, 64 of fp32)
   const int64_t padded = (cols / kChunk + 3) & ~int64_t{3};
-  const int threads = static_cast<int>(std::min<int64_t>(256, (padded + 31) / 32 * 32));
-  const int64_t u = (padded + threads - 1) / threads;
-  auto kern = u <= 1   ? k_fp4_quantize_nv<BF16, 1>
-              : u <= 2 ? k_fp4_quantize_nv<BF16, 2>
-              : u <= 4 ? k_fp4_quantize_nv<BF16, 4>
+  const int u = padded <= 256 ? 1 : padded <= 1024 ? 2 : padded <= 2048 && BF16 ? 4 : 0;
+  const int threads = u == 0 ? 512 : static_cast<int>(((padded + u - 1) / u + 31) / 32 * 32);
+  auto kern = u == 1   ? k_fp4_quantize_nv<BF16, 1>
+              : u == 2 ? k_fp4_quantize_nv<BF16, 2>
+              : u == 4 ? k_fp4_quantize_nv<BF16, BF16 ? 4 : 0>
                        : k_fp4_quantize_nv<BF16, 0>;
   return launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, st, X, cols, codes,
                     scales, gscale);
@@ -384,7 +495,7 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
 template <bool BF16>
 cudaError_t quantize_weight(const void* W, int64_t n, int64_t k, int format, const Fp4Out& w,
                             const Fp4Out& wt, uint32_t* top, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((k + 63) / 64), static_cast<unsigned>((n + 63) / 64));
+  const dim3 grid(static_cast<unsigned>((k + 511) / 512), static_cast<unsigned>(n / 32));
   if (format == QLORA_FP4_MX)
     return launch_pdl(k_fp4_quantize_weight<Fp4::kMx, BF16>, grid, dim3(256), 0, st, W, n, k,
                       static_cast<const uint32_t*>(nullptr), w.codes, w.scales, w.gscale, wt.codes,
@@ -423,13 +534,13 @@ cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int6
 }
 
 cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st) {
-  const int64_t total = q.rows * (q.cols / 8);
-  const int64_t blocks = std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(num_sms()) * 16);
+  const dim3 grid(static_cast<unsigned>((q.rows + 7) / 8),
+                  static_cast<unsigned>(std::min((q.cols + 1023) / 1024, kMaxGridY)));
   auto kern = q.format == QLORA_FP4_MX
                   ? (bf16 ? k_fp4_dequant<Fp4::kMx, true> : k_fp4_dequant<Fp4::kMx, false>)
                   : (bf16 ? k_fp4_dequant<Fp4::kNv, true> : k_fp4_dequant<Fp4::kNv, false>);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, q.codes, q.scales,
-                    q.gscale, q.gscale_rows > 1, q.rows, q.cols, fp4_ktiles(q.cols, q.format), out);
+  return launch_pdl(kern, grid, dim3(256), 0, st, q.codes, q.scales, q.gscale, q.gscale_rows > 1,
+                    static_cast<uint32_t>(q.rows), q.cols, fp4_ktiles(q.cols, q.format), out);
 }
 
 }  // namespace qlora

@@ -3,6 +3,9 @@
 #pragma once
 
 #include <cstdint>
+#include <cstring>
+
+#include <cuda_fp16.h>
 
 #include "internal.h"
 #include "sm100.cuh"
@@ -45,16 +48,17 @@ __device__ __forceinline__ uint32_t fp4_pack8(const float (&v)[8]) {
   return d;
 }
 
-// Eight E2M1 codes -> four pairs of fp16 values (exact), pair i holding codes 2i, 2i + 1.
-__device__ __forceinline__ void fp4_unpack8(uint32_t w, uint32_t (&h)[4]) {
+// The two E2M1 codes of a byte (bits 0-7 of w) as fp32 values.
+__device__ __forceinline__ float2 e2m1_pair(uint32_t w) {
+  uint32_t h;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      "mov.b32 {b0, b1, b2, b3}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+      : "=r"(h)
       : "r"(w));
+  __half2 v;
+  memcpy(&v, &h, 4);
+  return __half22float2(v);
 }
 
 // fp32 -> E4M3 bits (nearest, ties to even, 448 at most).
@@ -71,9 +75,9 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t b) {
     return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
-  float f;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
-  return f;
+  __half2 v;
+  memcpy(&v, &h, 4);
+  return __low2float(v);
 }
 
 // Scale byte of a block that holds a NaN or an infinity.
@@ -91,16 +95,6 @@ __device__ __forceinline__ int nv_gscale_exp(uint32_t top) {
 // 2^e for -127 <= e <= 127.
 __device__ __forceinline__ float pow2_f32(int e) {
   return __uint_as_float(e == -127 ? 0x00400000u : static_cast<uint32_t>(e + 127) << 23);
-}
-
-// Magnitude bits of x, 0 and `bad` set for NaN and infinities (they never enter a maximum).
-__device__ __forceinline__ uint32_t finite_mag(float x, bool& bad) {
-  const uint32_t m = __float_as_uint(x) & 0x7FFFFFFFu;
-  if (m >= 0x7F800000u) {
-    bad = true;
-    return 0u;
-  }
-  return m;
 }
 
 }  // namespace qlora

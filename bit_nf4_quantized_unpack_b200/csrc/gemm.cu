@@ -840,7 +840,7 @@ struct SplitPlan {
   int64_t tiles, rows_pad;
 };
 
-SplitPlan plan_split(int64_t rows, int64_t contraction) {
+SplitPlan plan_split_search(int64_t rows, int64_t contraction) {
   SplitPlan p;
   p.tiles = (rows + 127) / 128;
   p.rows_pad = p.tiles * 128;
@@ -867,6 +867,26 @@ SplitPlan plan_split(int64_t rows, int64_t contraction) {
     }
   }
   return p;
+}
+
+// The search takes a microsecond or two and every call asks for the same few plans several
+// times (workspace query, layout, launch): this thread's last ones are kept.
+SplitPlan plan_split(int64_t rows, int64_t contraction) {
+  struct Entry {
+    int64_t rows, contraction;
+    int sms;
+    SplitPlan plan;
+  };
+  constexpr int kEntries = 8;
+  thread_local Entry kept[kEntries] = {};
+  thread_local int next = 0;
+  const int sms = num_sms();
+  for (const Entry& e : kept)
+    if (e.sms == sms && e.rows == rows && e.contraction == contraction) return e.plan;
+  Entry& e = kept[next];
+  next = (next + 1) % kEntries;
+  e = Entry{rows, contraction, sms, plan_split_search(rows, contraction)};
+  return e.plan;
 }
 
 // Largest partial buffer (floats) the plans of one call may need.

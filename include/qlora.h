@@ -454,7 +454,7 @@ size_t qlora_fp4_quantize_weight_workspace_size(void);
  *   codes, scales       W [n_out, k_in]
  *   t_codes, t_scales   W^T [k_in, n_out], both NULL to leave it out
  *   gscale fp32 [1]     of both (NV; may be NULL for MX)
- * Errors: QLORA_ERR_SHAPE unless n_out and k_in are multiples of 32, at least 32, n_out <= 2^22 - 64
+ * Errors: QLORA_ERR_SHAPE unless n_out and k_in are multiples of 32, at least 32, n_out <= 65535 * 32
  * and n_out * k_in <= 2^40; otherwise those of qlora_fp4_quantize and QLORA_ERR_WORKSPACE.
  */
 qlora_status qlora_fp4_quantize_weight(const void *W, qlora_dtype w_dtype, int64_t n_out,
