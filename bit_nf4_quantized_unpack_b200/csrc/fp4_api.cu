@@ -135,7 +135,8 @@ qlora_status qlora_fp4_matmul(qlora_fp4_matrix a, qlora_fp4_matrix b, qlora_dtyp
   if (!is_aligned16(out)) return QLORA_ERR_ALIGN;
   q = check_device();
   if (q != QLORA_OK) return q;
-  return fp4_product(a, b, nullptr, out, out_dtype == QLORA_F32, static_cast<cudaStream_t>(stream));
+  return fp4_product(a, b, nullptr, out, out_dtype == QLORA_F32, false,
+                     static_cast<cudaStream_t>(stream));
 }
 
 size_t qlora_fp4_linear_fwd_workspace_size(int64_t M, int64_t n_out, int64_t k_in, int r,

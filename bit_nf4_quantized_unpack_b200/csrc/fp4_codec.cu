@@ -91,6 +91,12 @@ __device__ __forceinline__ uint32_t finite_amax(const R& r) {
   return m;
 }
 
+// The two bf16 values of a word.
+__device__ __forceinline__ void expand2(uint32_t w, float* v) {
+  v[0] = __uint_as_float(w << 16);
+  v[1] = __uint_as_float(w & 0xFFFF0000u);
+}
+
 // x / d for positive normal d, correctly rounded: the reciprocal's product and one correction
 // by its exact remainder. (Results below the normal range only round to the code 0.)
 __device__ __forceinline__ float div_rn(float x, float d, float rcp) {
@@ -254,6 +260,176 @@ __global__ void __launch_bounds__(512)
     }
   }
 }
+
+// One row by a CTA of 256 threads, in passes of four chunks a thread; a row that fits one pass
+// stays in registers between the maximum and the codes.
+template <Fp4 F>
+__device__ __forceinline__ void quantize_row(const uint16_t* __restrict__ X, int64_t row, int64_t cols,
+                                             uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                             float* __restrict__ gscale, uint32_t* part) {
+  constexpr int U = 4, NT = 256;
+  constexpr int kGroup = 4 * kFp4Block<F> / kChunk;  // chunks of four blocks
+  const int tid = threadIdx.x;
+  const int chunks = static_cast<int>(cols / kChunk), padded = (chunks + kGroup - 1) / kGroup * kGroup;
+  Raw16<true> raw[U];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = base + tid + u * NT;
+      if (c < chunks) raw[u].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
+      else raw[u].zero();
+    }
+  };
+  fetch(0);
+  float g_inv = 1.f;
+  if constexpr (F == Fp4::kNv) {
+    uint32_t top = 0u;
+    for (int base = 0;;) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t m = raw[u].amax();
+        if (m >= kInf) m = finite_amax(raw[u]);
+        top = max(top, m);
+      }
+      base += U * NT;
+      if (base >= chunks) break;
+      fetch(base);
+    }
+    top = __reduce_max_sync(~0u, top);
+    if ((tid & 31) == 0) part[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) top = max(top, part[w]);
+    const int e = nv_gscale_exp(top);
+    if (tid == 0) gscale[row] = pow2_f32(e);
+    g_inv = pow2_f32(-e);
+    if (chunks > U * NT) fetch(0);
+  }
+  for (int base = 0; base < padded; base += U * NT) {
+    if (base > 0) fetch(base);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = base + tid + u * NT;
+      if (base + u * NT >= padded) break;  // the same in every thread
+      uint32_t am = raw[u].amax();
+      if (F == Fp4::kMx) am = max(am, __shfl_xor_sync(~0u, am, 1));
+      const uint32_t sb = c < chunks ? scale_byte<F>(am, g_inv) : 0u;
+      if (c < chunks)
+        *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<int64_t>(c) * (kChunk / 2)) =
+            codes16<F>(raw[u], sb, g_inv);
+      const uint32_t w = gather4<F>(sb);
+      if (c % kGroup == 0 && c < padded)
+        *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, c * kChunk / kFp4Block<F>, padded / kGroup)) = w;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ few tokens: X and T = X A
+// One launch for what a few tokens need before their product with the weight, in clusters of
+// eight CTAs. The first ceil(M / 8) clusters quantize one row per CTA. The others take 16
+// tokens, 16 columns of A and 4096 rows of it (512 per CTA, 64 per warp, fetched at once:
+// the time is two memory latencies), multiply with mma.sync, and add up warps and then CTAs
+// in a fixed order, the CTAs through distributed shared memory. The product kernel adds the
+// parts of K above 4096.
+constexpr int kPrepThreads = 256;
+constexpr int kPrepTok = 16, kPrepCols = 16;
+constexpr int kPrepSlice = 512;                    // rows of A per CTA
+constexpr int kPrepXPitch = kPrepSlice * 2 + 16;   // bytes; conflict-free for ldmatrix
+constexpr int kPrepAPitch = kPrepCols * 2 + 16;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <Fp4 F>
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
+    k_fp4_prep(const uint16_t* __restrict__ X, int M, int64_t K, uint8_t* __restrict__ codes,
+               uint8_t* __restrict__ scales, float* __restrict__ gscale,
+               const uint16_t* __restrict__ A, int r, float* __restrict__ T) {
+  griddep_wait_and_release();
+  __shared__ uint32_t part[16];
+  __shared__ __align__(16) uint8_t xs[kPrepTok * kPrepXPitch];
+  __shared__ __align__(16) uint8_t as[kPrepSlice * kPrepAPitch];
+  __shared__ float mine[kPrepTok * kPrepCols];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row_ctas = (M + 7) / 8 * 8;
+  if (static_cast<int>(blockIdx.x) < row_ctas) {
+    if (static_cast<int>(blockIdx.x) < M)
+      quantize_row<F>(X, blockIdx.x, K, codes, scales, gscale, part);
+    return;  // the whole cluster takes this branch: its barrier is not used
+  }
+  const int jobs_j = (r + kPrepCols - 1) / kPrepCols, jobs_t = (M + kPrepTok - 1) / kPrepTok;
+  const int job = (blockIdx.x - row_ctas) / 8, rank = blockIdx.x & 7;
+  const int j0 = job % jobs_j * kPrepCols, t0 = job / jobs_j % jobs_t * kPrepTok;
+  const int kpart = job / (jobs_j * jobs_t);
+  const int64_t k0 = (static_cast<int64_t>(kpart) * 8 + rank) * kPrepSlice;
+  const uint32_t xs_s = smem_u32(xs), as_s = smem_u32(as);
+#pragma unroll
+  for (int u = 0; u < kPrepSlice * 2 / kPrepThreads; ++u) {  // A: two 16-byte pieces a row
+    const int i = tid + u * kPrepThreads, k = i >> 1, j = (i & 1) * 8;
+    const bool in = k0 + k < K && j0 + j < r;
+    cp_async16(as_s + k * kPrepAPitch + j * 2, in ? A + (k0 + k) * r + j0 + j : A, in);
+  }
+#pragma unroll
+  for (int u = 0; u < kPrepTok * kPrepSlice / 8 / kPrepThreads; ++u) {
+    const int i = tid + u * kPrepThreads, t = i / (kPrepSlice / 8), k = i % (kPrepSlice / 8) * 8;
+    const bool in = t0 + t < M && k0 + k < K;
+    cp_async16(xs_s + t * kPrepXPitch + k * 2, in ? X + (t0 + t) * K + k0 + k : X, in);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  float acc[2][4] = {};
+#pragma unroll
+  for (int i = 0; i < kPrepSlice / 8 / 16; ++i) {
+    const int k = warp * (kPrepSlice / 8) + i * 16;
+    uint32_t a[4], b[4];
+    ldmatrix_x4(xs_s + (lane & 15) * kPrepXPitch + (k + (lane >> 4) * 8) * 2, a);
+    ldmatrix_x4_trans(as_s + (k + (lane & 15)) * kPrepAPitch + (lane >> 4) * 16, b);
+    mma_16816(acc[0], a, b[0], b[1]);
+    mma_16816(acc[1], a, b[2], b[3]);
+  }
+  __syncthreads();  // the tokens have been read: their memory takes the warps' sums
+  float* sums = reinterpret_cast<float*>(xs);  // [8][16 tokens][16]
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      sums[warp * 256 + ((lane >> 2) + (e >> 1) * 8) * 16 + h * 8 + (lane & 3) * 2 + (e & 1)] = acc[h][e];
+  __syncthreads();
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) v += sums[w * 256 + tid];
+  mine[tid] = v;
+  cluster_sync_all();
+  if (rank == 0) {
+    v = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v += ld_cluster_f32(mine + tid, c);
+    const int t = t0 + (tid >> 4), j = j0 + (tid & 15);
+    if (t < M && j < r) T[(static_cast<int64_t>(kpart) * M + t) * r + j] = v;
+  }
+  cluster_sync_all();  // no CTA leaves while its sums are being read
+}
+static_assert(kPrepTok * kPrepCols == kPrepThreads && 8 * 256 * 4 <= kPrepTok * kPrepXPitch, "sums");
 
 // ------------------------------------------------------------------ weights, square blocks
 // Largest finite magnitude of the matrix, as fp32 bits in *top (zero before the launch).
@@ -531,6 +707,18 @@ cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int6
   uint32_t* top = static_cast<uint32_t*>(ws);
   return bf16 ? quantize_weight<true>(W, n, k, format, w, wt, top, st)
               : quantize_weight<false>(W, n, k, format, w, wt, top, st);
+}
+
+int fp4_prep_parts(int64_t K) { return static_cast<int>((K + 8 * kPrepSlice - 1) / (8 * kPrepSlice)); }
+
+cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out& out,
+                            const uint16_t* A, int r, float* T, cudaStream_t st) {
+  const int m = static_cast<int>(M);
+  const int jobs = (m + kPrepTok - 1) / kPrepTok * ((r + kPrepCols - 1) / kPrepCols) * fp4_prep_parts(K);
+  const dim3 grid((m + 7) / 8 * 8 + 8 * jobs);
+  auto kern = format == QLORA_FP4_MX ? k_fp4_prep<Fp4::kMx> : k_fp4_prep<Fp4::kNv>;
+  return launch_pdl(kern, grid, dim3(kPrepThreads), 0, st, X, m, K, out.codes, out.scales, out.gscale,
+                    A, r, T);
 }
 
 cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st) {

@@ -37,55 +37,70 @@ struct Fp4Args {
 };
 
 // ------------------------------------------------------------------ split kernel
-// One tile of 128 weight rows x NT tokens per CTA; the `cs` CTAs of a cluster take parts of K
-// and add their accumulators through distributed shared memory in rank order.
-// Warp 0: TMA, warp 1: MMA and TMEM, warps 2-5: epilogue.
+// Few tokens (Q <= NT): reading the weight once bounds the time. A CTA takes 128 weight rows and
+// all tokens; the `cs` CTAs of a cluster share the steps over K, put their accumulators in
+// shared memory and each add up a part of the tokens through distributed shared memory, in
+// rank order.
+//
+// With the rank-r term, `t` holds the fp32 [Q, r] values in parts; rank 0's epilogue warps add
+// them and turn them into the bf16 hi and lo operands in shared memory.
+//
+// Launched behind a kernel that itself waited for everything before it (`early`), the CTAs
+// fetch their first weight tiles before they wait for the tokens.
+//
+// Warp 0: TMA, warp 1: MMA and tensor memory, warps 2-5: epilogue. Tensor memory: an
+// accumulator of NT columns, then 32 scale columns for each slot of the ring.
 constexpr int kSplitThreads = 192;
-constexpr int split_nq(int nt) { return (nt + 127) / 128; }  // scale row tiles of the tokens
-constexpr int split_stages(int nt) { return nt <= 64 ? 4 : nt <= 128 ? 5 : 4; }
-constexpr uint32_t split_stage_bytes(int nt) { return kPBytes + nt * 128; }
-constexpr uint32_t split_sf_bytes(int nt) { return 4 * kSfTile * (1 + split_nq(nt)); }
-constexpr uint32_t split_smem(int nt) {
-  return 1024 + split_stages(nt) * (split_stage_bytes(nt) + split_sf_bytes(nt)) + 256;
+constexpr uint32_t split_slot_bytes(int nt) { return kPBytes + nt * 128 + 8 * kSfTile; }
+constexpr uint32_t split_smem(int nt, int slots) {
+  return 1024 + slots * split_slot_bytes(nt) + 2 * nt * 128 + 512;
 }
-constexpr uint32_t split_set_cols(int nt) { return 16 + 16 * split_nq(nt); }
-constexpr uint32_t split_tmem(int nt) {
-  return nt + 2 * split_set_cols(nt) <= 128 ? 128 : nt + 2 * split_set_cols(nt) <= 256 ? 256 : 512;
-}
+constexpr int kSplitMaxSlots = 8;
+
+struct SplitArgs {
+  int cs;           // CTAs of a cluster
+  int slots;        // of the ring, at most kSplitMaxSlots
+  uint32_t tmem;    // columns to allocate
+  const float* t;   // [t_parts][Q, r] fp32 or NULL
+  int t_parts;
+  float* t_out;     // [Q, r] or NULL: their sum
+  int r;
+  float scale;
+  bool early;
+};
 
 template <Fp4 F, int NT>
-__global__ void __launch_bounds__(kSplitThreads, 1)
+__global__ void __launch_bounds__(kSplitThreads)
     k_fp4_gemm_split(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
-                     const __grid_constant__ CUtensorMap tm_ext_p,
-                     const __grid_constant__ CUtensorMap tm_ext_q, const Fp4Args args, const int cs) {
-  constexpr int S = split_stages(NT);
-  constexpr int NQ = split_nq(NT);
+                     const __grid_constant__ CUtensorMap tm_ext_p, const Fp4Args args,
+                     const SplitArgs sa) {
   constexpr uint32_t kQBytes = NT * 128;
   constexpr int kTileStep = kStepCols / kFp4TileCols<F>;  // scale tiles per step: 2 or 4
   constexpr int kMmaTile = 4 / kTileStep;                 // MMAs per scale tile: 2 or 1
-  constexpr uint32_t kSet = split_set_cols(NT);
+  const int S = sa.slots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* p_s = smem;                         // [S][kPBytes]
   uint8_t* q_s = p_s + S * kPBytes;            // [S][kQBytes]
-  uint8_t* sfp_s = q_s + S * kQBytes;          // [S][4][512]
-  uint8_t* sfq_s = sfp_s + S * 4 * kSfTile;    // [S][NQ][4][512]
-  uint64_t* full = reinterpret_cast<uint64_t*>(sfq_s + S * NQ * 4 * kSfTile);
-  uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  uint8_t* ext_s = q_s + S * kQBytes;          // [2][kQBytes] rank-r token operand, hi | lo
+  uint8_t* sfp_s = ext_s + 2 * kQBytes;        // [S][4][512]
+  uint8_t* sfq_s = sfp_s + S * 4 * kSfTile;    // [S][4][512]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sfq_s + S * 4 * kSfTile);
+  uint64_t* empty = full + kSplitMaxSlots;
+  uint64_t* acc_full = empty + kSplitMaxSlots;
+  uint64_t* ext_ready = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ext_ready + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = sa.cs;
   const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / cs;
-  const int64_t p0 = static_cast<int64_t>(tile % args.p_tiles) * kPRows;
-  const int64_t q0 = static_cast<int64_t>(tile / args.p_tiles) * NT;
   const int s_begin = static_cast<int>(static_cast<int64_t>(args.steps) * rank / cs);
-  const int s_end = static_cast<int>(static_cast<int64_t>(args.steps) * (rank + 1) / cs);
-  const int nmain = s_end - s_begin;
-  const int nsteps = nmain + (rank == 0 && args.ext_mmas > 0 ? 2 : 0);
+  const int nmain = static_cast<int>(static_cast<int64_t>(args.steps) * (rank + 1) / cs) - s_begin;
+  const bool ext = rank == 0 && args.ext_mmas > 0;  // one more step, after the others
+  const int nsteps = nmain + ext;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -93,173 +108,212 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(acc_full, 1);
+    mbar_init(ext_ready, 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, split_tmem(NT));
+    tmem_alloc(tmem_slot, sa.tmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_d = *tmem_slot;
-  griddep_wait_and_release();
+  const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     if (elect_one()) {
-      int issued = 0;
-      const int64_t prow_tile = p0 / 128, qrow_tile = q0 / 128;
-      const int nq = (NQ == 2 && args.Q - q0 > 128) ? 2 : 1;  // token scale tiles that exist
+      const int p0 = tile * kPRows;
+      auto load_weight = [&](int i, int s) {
+        uint8_t* dst = p_s + s * kPBytes;
+        if (i < nmain) {
+          const int step = s_begin + i, t0 = step * kTileStep;
+          const uint32_t sf = static_cast<uint32_t>(min(kTileStep, args.ktiles - t0)) * kSfTile;
+          mbar_arrive_expect_tx(&full[s], kPBytes + kQBytes + 2 * sf);
+          tma_load_2d(dst, &tm_p, &full[s], step * 128, p0);
+          bulk_load(sfp_s + s * 4 * kSfTile, args.sp + (static_cast<int64_t>(tile) * args.ktiles + t0) * kSfTile,
+                    sf, &full[s]);
+        } else {
+          mbar_arrive_expect_tx(&full[s], kPBytes);
+          if (args.ext_mn) {
+            tma_load_2d(dst, &tm_ext_p, &full[s], p0, 0);
+            tma_load_2d(dst + 8192, &tm_ext_p, &full[s], p0 + 64, 0);
+          } else {
+            tma_load_2d(dst, &tm_ext_p, &full[s], 0, p0);
+          }
+        }
+      };
+      const int ahead = sa.early ? min(S, nsteps) : 0;
+      for (int i = 0; i < ahead; ++i) load_weight(i, i);
+      griddep_wait_and_release();
+      int issued = 0, s = 0;
+      uint32_t phase = 1;  // of empty[s] before its latest use
       for (int i = 0; i < nsteps; ++i) {
-        const int s = i % S;
-        if (i >= S && !mbar_wait(&empty[s], ((i / S) - 1) & 1u, abort_flag)) {
+        if (i >= S && !mbar_wait(&empty[s], phase, abort_flag)) {
           record_error(args.err, abort_flag, kErrTimeoutProducer);
           break;
         }
+        if (i >= ahead) load_weight(i, s);
         if (i < nmain) {
-          const int step = s_begin + i;
-          const int t0 = step * kTileStep;
-          const uint32_t sf = static_cast<uint32_t>(min(kTileStep, args.ktiles - t0)) * kSfTile;
-          mbar_arrive_expect_tx(&full[s], kPBytes + kQBytes + sf * (1 + nq));
-          tma_load_2d(p_s + s * kPBytes, &tm_p, &full[s], step * 128, static_cast<int>(p0));
-          tma_load_2d(q_s + s * kQBytes, &tm_q, &full[s], step * 128, static_cast<int>(q0));
-          bulk_load(sfp_s + s * 4 * kSfTile, args.sp + (prow_tile * args.ktiles + t0) * kSfTile, sf,
-                    &full[s]);
-          for (int h = 0; h < nq; ++h)
-            bulk_load(sfq_s + (s * NQ + h) * 4 * kSfTile,
-                      args.sq + ((qrow_tile + h) * args.ktiles + t0) * kSfTile, sf, &full[s]);
-        } else {
-          // bf16 extension: hi part, then lo part of the token operand; columns past r are 0
-          mbar_arrive_expect_tx(&full[s], kPBytes + kQBytes);
-          if (args.ext_mn) {
-            tma_load_2d(p_s + s * kPBytes, &tm_ext_p, &full[s], static_cast<int>(p0), 0);
-            tma_load_2d(p_s + s * kPBytes + 8192, &tm_ext_p, &full[s], static_cast<int>(p0) + 64, 0);
-          } else {
-            tma_load_2d(p_s + s * kPBytes, &tm_ext_p, &full[s], 0, static_cast<int>(p0));
-          }
-          tma_load_2d(q_s + s * kQBytes, &tm_ext_q, &full[s], (i - nmain) * 64, static_cast<int>(q0));
+          const int step = s_begin + i, t0 = step * kTileStep;
+          tma_load_2d(q_s + s * kQBytes, &tm_q, &full[s], step * 128, 0);
+          bulk_load(sfq_s + s * 4 * kSfTile, args.sq + static_cast<int64_t>(t0) * kSfTile,
+                    static_cast<uint32_t>(min(kTileStep, args.ktiles - t0)) * kSfTile, &full[s]);
         }
         ++issued;
+        if (++s == S) s = 0, phase ^= 1;
       }
       if (*abort_flag)
-        for (int i = max(0, issued - S); i < issued; ++i)
-          mbar_wait_drain(&full[i % S], (i / S) & 1u);
+        for (int i = max(0, issued - S); i < issued; ++i) mbar_wait_drain(&full[i % S], (i / S) & 1u);
     }
   } else if (warp == 1) {
+    griddep_wait_and_release();
     if (elect_one()) {
       const uint32_t idesc_ext = idesc_bf16_f32(kPRows, NT, args.ext_mn, false);
+      int done = 0, s = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      int done = 0;
-      for (int i = 0; i < nsteps && ok; ++i) {
-        const int s = i % S;
-        ok = mbar_wait(&full[s], (i / S) & 1u, abort_flag);
-        // The scale columns of step i were last read by the MMAs of step i - 2 (two sets, used
-        // in turn), and MMAs of different kinds are not ordered with each other: wait for the
-        // completion of step i - 2, and for step i - 1 where the kind changes.
-        if (ok && i < nmain && i >= 2)
-          ok = mbar_wait(&empty[(i - 2) % S], ((i - 2) / S) & 1u, abort_flag);
-        if (ok && i == nmain && i >= 1)
-          ok = mbar_wait(&empty[(i - 1) % S], ((i - 1) / S) & 1u, abort_flag);
+      for (int i = 0; i < nsteps; ++i) {
+        ok = mbar_wait(&full[s], phase, abort_flag);
+        // MMAs of different kinds are not ordered with each other: before the rank-r step, wait
+        // for the completion of the one before. (Every ring slot has its own scale columns, so
+        // a slot that is full again has had its columns read.)
+        if (ok && i == nmain) {
+          ok = mbar_wait(ext_ready, 0, abort_flag);
+          if (ok && i >= 1) ok = mbar_wait(&empty[(i - 1) % S], ((i - 1) / S) & 1u, abort_flag);
+        }
         if (!ok) {
           record_error(args.err, abort_flag, kErrTimeoutMma);
           break;
         }
         tc_fence_after();
-        const uint32_t pa = smem_u32(p_s + s * kPBytes), qa = smem_u32(q_s + s * kQBytes);
-        const uint64_t dq = smem_desc_sw128(qa, 16, 1024);
+        const uint32_t pa = smem_u32(p_s + s * kPBytes);
         if (i < nmain) {
           const uint64_t dp = smem_desc_sw128(pa, 16, 1024);
-          const uint32_t sfp = tmem_d + NT + (i & 1) * kSet, sfq = sfp + 16;
+          const uint64_t dq = smem_desc_sw128(smem_u32(q_s + s * kQBytes), 16, 1024);
+          const uint32_t sfp = tmem + NT + s * 32, sfq = sfp + 16;
+          const uint32_t sp = smem_u32(sfp_s + s * 4 * kSfTile), sq = smem_u32(sfq_s + s * 4 * kSfTile);
           const int64_t left = args.K - static_cast<int64_t>(s_begin + i) * kStepCols;
           const int mmas = left >= kStepCols ? 4 : static_cast<int>((left + 63) / 64);
-          for (int kk = 0; kk < mmas; ++kk) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= mmas) break;
             const int t = kk / kMmaTile, sub = kk % kMmaTile;
             if (sub == 0) {
-              tmem_cp_scales(sfp + t * 4, smem_desc_scales(smem_u32(sfp_s + (s * 4 + t) * kSfTile)));
-              for (int h = 0; h < NQ; ++h)
-                tmem_cp_scales(sfq + (t * NQ + h) * 4,
-                               smem_desc_scales(smem_u32(sfq_s + ((s * NQ + h) * 4 + t) * kSfTile)));
+              tmem_cp_scales(sfp + t * 4, smem_desc_scales(sp + t * kSfTile));
+              tmem_cp_scales(sfq + t * 4, smem_desc_scales(sq + t * kSfTile));
             }
             umma_fp4<F == Fp4::kMx ? 2 : 4>(
-                tmem_d, dp + kk * 2u, dq + kk * 2u,
+                tmem, dp + kk * 2u, dq + kk * 2u,
                 idesc_fp4(kPRows, NT, F == Fp4::kMx, F == Fp4::kMx ? 2 * sub : 0), sfp + t * 4,
-                sfq + t * NQ * 4, (i | kk) != 0);
+                sfq + t * 4, (i | kk) != 0);
           }
         } else {
           const uint64_t dp = args.ext_mn ? smem_desc_sw128(pa, 8192, 1024) : smem_desc_sw128(pa, 16, 1024);
           const uint32_t adv = args.ext_mn ? 128u : 2u;
-          for (int kk = 0; kk < args.ext_mmas; ++kk)
-            umma_bf16(tmem_d, dp + kk * adv, dq + kk * 2u, idesc_ext, (i | kk) != 0);
+          for (int part = 0; part < 2; ++part) {
+            const uint64_t dq = smem_desc_sw128(smem_u32(ext_s + part * kQBytes), 16, 1024);
+            for (int kk = 0; kk < args.ext_mmas; ++kk)
+              umma_bf16(tmem, dp + kk * adv, dq + kk * 2u, idesc_ext, (i | part | kk) != 0);
+          }
         }
         umma_commit(&empty[s]);
         ++done;
+        if (++s == S) s = 0, phase ^= 1;
       }
       umma_commit(acc_full);
       mbar_wait_drain(acc_full, 0);
       uint32_t par;
-      for (int s = 0; s < S; ++s)
-        if (last_use(done, S, s, par)) mbar_wait_drain(&empty[s], par);
+      for (int j = 0; j < S; ++j)
+        if (last_use(done, S, j, par)) mbar_wait_drain(&empty[j], par);
     }
   } else {
+    griddep_wait_and_release();
+    const int quarter = warp & 3, tid = threadIdx.x - 64;
+    const int Q = static_cast<int>(args.Q);
+    if (ext) {
+      // scale t / (ga gb) as bf16 hi and lo parts in the K-major swizzled operand layout
+      const float gb = args.gp ? *args.gp : 1.f;
+#pragma unroll 4
+      for (int i = tid; i < NT * 8; i += 128) {  // eight values of a token: one 16-byte group
+        const int q = i >> 3, j = (i & 7) * 8;
+        float v[8] = {};
+        if (q < Q && j < sa.r) {
+          const float ga = args.gq ? __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
+#pragma unroll 4
+          for (int part = 0; part < sa.t_parts; ++part) {
+            const float4* src =
+                reinterpret_cast<const float4*>(sa.t + (static_cast<int64_t>(part) * Q + q) * sa.r + j);
+            const float4 x = __ldg(src), y = __ldg(src + 1);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+          }
+          if (sa.t_out && tile == 0) {
+            float4* dst = reinterpret_cast<float4*>(sa.t_out + static_cast<int64_t>(q) * sa.r + j);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = v[k] * sa.scale / ga / gb;
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          hi[k] = pack_bf16x2_rn(v[2 * k], v[2 * k + 1]);
+          lo[k] = pack_bf16x2_rn(v[2 * k] - __uint_as_float(hi[k] << 16),
+                                 v[2 * k + 1] - __uint_as_float(hi[k] & 0xFFFF0000u));
+        }
+        const uint32_t off = sw128_kmajor_offset(q, i & 7);
+        *reinterpret_cast<uint4*>(ext_s + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(ext_s + kQBytes + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ext_ready);
+    }
+    // this CTA's tokens (a share of the cluster's), and this lane's four rows of every fourth
+    const int span = (Q + cs - 1) / cs, t0 = min(Q, rank * span), t1 = min(Q, t0 + span);
+    const int r4 = quarter * 32 + (lane & 7) * 4;
+    const int64_t p4 = static_cast<int64_t>(tile) * kPRows + r4;
+    float g4[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      g4[j] = args.gp ? __ldg(args.gp + (args.gp_rows ? min(p4 + j, args.P - 1) : 0)) : 1.f;
     const bool got = mbar_wait(acc_full, 0, abort_flag) && !*abort_flag;
     if (!got && !*abort_flag) record_error(args.err, abort_flag, kErrTimeoutEpilogue);
     tc_fence_after();
-    const int quarter = warp & 3;
-    const int64_t p = p0 + quarter * 32 + lane;
-    const uint32_t taddr = tmem_d + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* part = reinterpret_cast<float*>(smem);  // [NT][128], over the consumed stages
-    const float gp = args.gp ? args.gp[args.gp_rows ? min(p, args.P - 1) : 0] : 1.f;
-    // value of (p, token q) -> output
-    auto store_pair = [&](int64_t q, float v0, float v1) {  // tokens q and q + 1
-      v0 *= gp;
-      v1 *= gp;
-      if (args.gq) {
-        v0 *= args.gq[args.gq_rows ? min(q, args.Q - 1) : 0];
-        v1 *= args.gq[args.gq_rows ? min(q + 1, args.Q - 1) : 0];
-      }
-      if (args.out_f32) {
-        float* o = static_cast<float*>(args.out) + q * args.ld + p;
-        if (p < args.P && q < args.Q) o[0] = v0;
-        if (p < args.P && q + 1 < args.Q) o[args.ld] = v1;
-      } else {
-        // even lanes write rows p, p + 1 of token q, odd lanes rows p - 1, p of token q + 1
-        const float got = __shfl_xor_sync(~0u, (lane & 1) ? v0 : v1, 1);
-        const int64_t tq = q + (lane & 1), tp = p & ~int64_t{1};
-        const uint32_t w = (lane & 1) ? pack_bf16x2_rn(got, v1) : pack_bf16x2_rn(v0, got);
-        if (tp < args.P && tq < args.Q)
-          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.out) + tq * args.ld + tp) = w;
-      }
-    };
+    // every step has been multiplied, so the ring is free: sums as [token][128 rows]
+    float* part = reinterpret_cast<float*>(smem);
     if (got) {
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
-      for (int c = 0; c < NT / 32; ++c) {
+      for (int c = 0; c * 32 < Q; ++c) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(taddr + c * 32, v);
         tmem_ld_wait();
-        if (cs > 1) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) part[(c * 32 + j) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
-        } else if (q0 + c * 32 < args.Q) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            store_pair(q0 + c * 32 + j, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-        }
+        for (int j = 0; j < 32; ++j) part[(c * 32 + j) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
       }
     }
-    if (cs > 1) {
-      cluster_sync_all();
-      // rank r sums and writes tokens [r, r + 1) NT / cs of the tile
-      const int span = NT / cs;
-      const int t0 = rank * span;
-      for (int t = t0; t < t0 + span; t += 2) {
-        if (q0 + t >= args.Q) break;
-        float v0 = 0.f, v1 = 0.f;
-        for (int r = 0; r < cs; ++r) {
-          v0 += ld_cluster_f32(part + t * 128 + quarter * 32 + lane, r);
-          v1 += ld_cluster_f32(part + (t + 1) * 128 + quarter * 32 + lane, r);
+    if (cs > 1) cluster_sync_all();
+    else __syncwarp();  // a warp reads only what it wrote
+    if (got) {
+      for (int q = t0 + (lane >> 3); q < t1; q += 4) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int c = 0; c < cs; ++c) {
+          const float4 v = ld_cluster_f32x4(part + q * 128 + r4, cs > 1 ? c : rank);
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
-        if (!*abort_flag) store_pair(q0 + t, v0, v1);
+        if (p4 >= args.P) continue;  // P is a multiple of 8
+        const float gq = args.gq ? __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
+        const float4 o = make_float4(sum.x * g4[0] * gq, sum.y * g4[1] * gq, sum.z * g4[2] * gq,
+                                     sum.w * g4[3] * gq);
+        if (args.out_f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(args.out) + q * args.ld + p4) = o;
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + q * args.ld + p4) =
+              make_uint2(pack_bf16x2_rn(o.x, o.y), pack_bf16x2_rn(o.z, o.w));
       }
     }
   }
@@ -272,7 +326,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_d, split_tmem(NT));
+    tmem_dealloc(tmem, sa.tmem);
   }
 }
 
@@ -612,37 +666,42 @@ constexpr CUtensorMapDataType kU8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 constexpr CUtensorMapDataType kBf16Map = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 constexpr CUtensorMapSwizzle kSw128 = CU_TENSOR_MAP_SWIZZLE_128B;
 
-// The extension's operand maps (boxes of 128 weight rows, q_box tokens); tp and tq stand in
-// when there is none.
-qlora_status ext_maps(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
-                      uint32_t q_box, CUtensorMap* xp, CUtensorMap* xq) {
-  if (!ext) return QLORA_OK;
-  if (ext->mn_major) QL_MAP(xp, kBf16Map, ext->p, b.rows, ext->r, b.rows * 2, 64, 64, kSw128);
-  else QL_MAP(xp, kBf16Map, ext->p, ext->r, b.rows, ext->r * 2, 64, kPRows, kSw128);
-  QL_MAP(xq, kBf16Map, ext->q, 128, a.rows, 256, 64, q_box, kSw128);
-  return QLORA_OK;
-}
-
 template <Fp4 F, int NT>
 qlora_status run_split(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
-                       Fp4Args args, int cs, cudaStream_t st) {
-  CUtensorMap tp, tq, xp, xq;
+                       const Fp4Args& args, bool early, cudaStream_t st) {
+  CUtensorMap tp, tq, xp;
   QL_MAP(&tp, kU8, b.codes, b.cols / 2, b.rows, b.cols / 2, 128, kPRows, kSw128);
   QL_MAP(&tq, kU8, a.codes, a.cols / 2, a.rows, a.cols / 2, 128, NT, kSw128);
   xp = tp;
-  xq = tq;
-  qlora_status q = ext_maps(a, b, ext, NT, &xp, &xq);
-  if (q != QLORA_OK) return q;
-  auto kern = k_fp4_gemm_split<F, NT>;
-  constexpr uint32_t smem = split_smem(NT);
-  QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  const int64_t tiles = static_cast<int64_t>(args.p_tiles) * ((a.rows + NT - 1) / NT);
-  if (tiles * cs > (int64_t{1} << 30)) {
-    set_last_error("the product has too many tiles");
-    return QLORA_ERR_SHAPE;
+  SplitArgs sa = {};
+  if (ext) {
+    if (ext->mn_major) QL_MAP(&xp, kBf16Map, ext->p, b.rows, ext->r, b.rows * 2, 64, 64, kSw128);
+    else QL_MAP(&xp, kBf16Map, ext->p, ext->r, b.rows, ext->r * 2, 64, kPRows, kSw128);
+    sa.t = ext->t;
+    sa.t_parts = ext->t_parts;
+    sa.t_out = ext->t_out;
+    sa.r = ext->r;
+    sa.scale = ext->scale;
   }
+  sa.early = early;
+  // One CTA per SM takes a ring as deep as fits; more than that share SMs in pairs, with half
+  // of shared and tensor memory each (NT = 128 leaves no room for a second).
+  const int deep = std::min<int>(kSplitMaxSlots, (227 * 1024 - split_smem(NT, 0)) / split_slot_bytes(NT));
+  const int half = std::min<int>(kSplitMaxSlots, (113 * 1024 - split_smem(NT, 0)) / split_slot_bytes(NT));
+  // as many CTAs a cluster as the SMs take at one time, with two steps each at least: two per
+  // SM read 3 to 12 % faster than one (8192 x 28672, one token: 24.7 against 26.8 us)
+  const int sms = num_sms(), at_once = half >= 3 ? 2 * sms : sms;
+  sa.cs = 1;
+  while (sa.cs < 8 && sa.cs * 4 <= args.steps && args.p_tiles * sa.cs * 2 <= at_once) sa.cs *= 2;
+  const int64_t ctas = static_cast<int64_t>(args.p_tiles) * sa.cs;
+  const bool pairs = ctas > sms && half >= 3;
+  sa.slots = pairs ? half : deep;
+  sa.tmem = NT + 32 * sa.slots <= 256 ? 256 : 512;
+  auto kern = k_fp4_gemm_split<F, NT>;
+  const uint32_t smem = split_smem(NT, sa.slots);
+  QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, split_smem(NT, deep)));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kSplitThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -650,13 +709,13 @@ qlora_status run_split(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, con
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.x = sa.cs;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 2 : 1;
+  cfg.numAttrs = sa.cs > 1 ? 2 : 1;
   note_launches(1);
-  QL_TRY(cudaLaunchKernelEx(&cfg, kern, tp, tq, xp, xq, args, cs));
+  QL_TRY(cudaLaunchKernelEx(&cfg, kern, tp, tq, xp, args, sa));
   return QLORA_OK;
 }
 
@@ -674,8 +733,11 @@ qlora_status run_pair(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, cons
   QL_MAP(&sq, kU64, a.scales, srow / 8, (a.rows + 127) / 128, srow, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
   xp = tp;
   xq = tq;
-  qlora_status q = ext_maps(a, b, ext, 128, &xp, &xq);
-  if (q != QLORA_OK) return q;
+  if (ext) {
+    if (ext->mn_major) QL_MAP(&xp, kBf16Map, ext->p, b.rows, ext->r, b.rows * 2, 64, 64, kSw128);
+    else QL_MAP(&xp, kBf16Map, ext->p, ext->r, b.rows, ext->r * 2, 64, kPRows, kSw128);
+    QL_MAP(&xq, kBf16Map, ext->q, 128, a.rows, 256, 64, 128, kSw128);
+  }
   if (args.out_f32)
     QL_MAP(&to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, args.out, b.rows, a.rows, b.rows * 4, 32, 32,
            CU_TENSOR_MAP_SWIZZLE_NONE);
@@ -696,25 +758,17 @@ qlora_status run_pair(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, cons
 
 template <Fp4 F>
 qlora_status run_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
-                         const Fp4Args& args, cudaStream_t st) {
-  const int64_t M = a.rows;
-  if (M > 128) return run_pair<F>(a, b, ext, args, st);
-  const int nt = M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  const int64_t tiles = static_cast<int64_t>(args.p_tiles) * ((M + nt - 1) / nt);
-  int cs = 1;
-  while (cs < 8 && cs * 2 <= args.steps && tiles * cs * 2 <= 2 * num_sms()) cs *= 2;
-  switch (nt) {
-    case 32: return run_split<F, 32>(a, b, ext, args, cs, st);
-    case 64: return run_split<F, 64>(a, b, ext, args, cs, st);
-    case 128: return run_split<F, 128>(a, b, ext, args, cs, st);
-    default: return run_split<F, 256>(a, b, ext, args, cs, st);
-  }
+                         const Fp4Args& args, bool early, cudaStream_t st) {
+  if (a.rows > kFp4SplitMaxM) return run_pair<F>(a, b, ext, args, st);
+  if (a.rows <= 32) return run_split<F, 32>(a, b, ext, args, early, st);
+  if (a.rows <= 64) return run_split<F, 64>(a, b, ext, args, early, st);
+  return run_split<F, 128>(a, b, ext, args, early, st);
 }
 
 }  // namespace
 
 qlora_status fp4_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
-                         void* out, bool out_f32, cudaStream_t st) {
+                         void* out, bool out_f32, bool early, cudaStream_t st) {
   Fp4Args args;
   args.sp = b.scales;
   args.sq = a.scales;
@@ -734,8 +788,8 @@ qlora_status fp4_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, c
   args.ld = b.rows;
   args.out_f32 = out_f32;
   args.err = device_error_word();
-  return a.format == QLORA_FP4_MX ? run_product<Fp4::kMx>(a, b, ext, args, st)
-                                  : run_product<Fp4::kNv>(a, b, ext, args, st);
+  return a.format == QLORA_FP4_MX ? run_product<Fp4::kMx>(a, b, ext, args, early, st)
+                                  : run_product<Fp4::kNv>(a, b, ext, args, early, st);
 }
 
 }  // namespace qlora

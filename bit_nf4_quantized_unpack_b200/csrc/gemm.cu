@@ -1298,16 +1298,24 @@ qlora_fp4_matrix carve_fp4(Carve& c, int64_t rows, int64_t cols, int format, Fp4
 }
 
 size_t fp4_fwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matrix* x, Fp4Out* xo,
-                      float** part, uint16_t** ts) {
+                      float** part, uint16_t** ts, float** t) {
   Carve c(ws);
   *x = carve_fp4(c, s.M, s.K, format, xo);
-  *part = c.take<float>(partial_floats(s.M, s.K, 64));
-  *ts = c.take<uint16_t>(static_cast<size_t>(s.M) * 128);
+  *part = nullptr;
+  *ts = nullptr;
+  *t = nullptr;
+  if (s.M > kFp4SplitMaxM) {
+    *part = c.take<float>(partial_floats(s.M, s.K, 64));
+    *ts = c.take<uint16_t>(static_cast<size_t>(s.M) * 128);
+  } else {
+    *t = c.take<float>(static_cast<size_t>(fp4_prep_parts(s.K)) * s.M * s.r);
+  }
   return c.off + 256;
 }
 
 size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matrix* y, Fp4Out* yo,
-                      float** part, uint16_t** gs, uint16_t** g3, uint16_t** t3, float** t) {
+                      float** part, uint16_t** gs, uint16_t** g3, uint16_t** t3, float** t,
+                      float** g) {
   Carve c(ws);
   *y = carve_fp4(c, s.M, s.N, format, yo);
   size_t pf = partial_floats(s.M, s.N, 64);                    // G = dY B^T
@@ -1318,6 +1326,7 @@ size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matr
   *g3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
   *t3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
   *t = c.take<float>(static_cast<size_t>(s.M) * s.r);
+  *g = c.take<float>(static_cast<size_t>(s.M) * s.r);
   return c.off + 256;
 }
 }  // namespace
@@ -1325,17 +1334,17 @@ size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matr
 size_t fp4_fwd_workspace(const LinearShape& s, int format) {
   qlora_fp4_matrix x;
   Fp4Out o;
-  float* p;
-  uint16_t* t;
-  return fp4_fwd_layout(s, format, nullptr, &x, &o, &p, &t);
+  float *p, *t;
+  uint16_t* ts;
+  return fp4_fwd_layout(s, format, nullptr, &x, &o, &p, &ts, &t);
 }
 
 size_t fp4_bwd_workspace(const LinearShape& s, int format) {
   qlora_fp4_matrix y;
   Fp4Out o;
-  float *p, *t;
+  float *p, *t, *g;
   uint16_t *gs, *g3, *t3;
-  return fp4_bwd_layout(s, format, nullptr, &y, &o, &p, &gs, &g3, &t3, &t);
+  return fp4_bwd_layout(s, format, nullptr, &y, &o, &p, &gs, &g3, &t3, &t, &g);
 }
 
 qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uint16_t* A,
@@ -1343,14 +1352,21 @@ qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uin
                          void* ws, cudaStream_t st) {
   qlora_fp4_matrix x;
   Fp4Out xo;
-  float* part;
+  float *part, *tbuf;
   uint16_t* ts;
-  fp4_fwd_layout(s, w.format, ws, &x, &xo, &part, &ts);
+  fp4_fwd_layout(s, w.format, ws, &x, &xo, &part, &ts, &tbuf);
+  Fp4Ext ext{B, nullptr, nullptr, 0, T_save, s.r, s.scale, true};
+  if (s.M <= kFp4SplitMaxM) {
+    QL_TRY(launch_fp4_prep(X, s.M, s.K, w.format, xo, A, s.r, tbuf, st));
+    ext.t = tbuf;
+    ext.t_parts = fp4_prep_parts(s.K);
+    return fp4_product(x, w, &ext, Y, false, true, st);
+  }
   QL_TRY(launch_fp4_quantize(X, true, s.M, s.K, w.format, xo, st));
   qlora_status q = lora_down_T(X, A, s, part, T_save, ts, st, x.gscale, w.gscale);
   if (q != QLORA_OK) return q;
-  const Fp4Ext ext{B, ts, s.r, true};
-  return fp4_product(x, w, &ext, Y, false, st);
+  ext.q = ts;
+  return fp4_product(x, w, &ext, Y, false, false, st);
 }
 
 qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_saved,
@@ -1359,9 +1375,9 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
                           cudaStream_t st) {
   qlora_fp4_matrix y;
   Fp4Out yo;
-  float *part, *tbuf;
+  float *part, *tbuf, *gbuf;
   uint16_t *gs, *g3, *t3;
-  fp4_bwd_layout(s, wt.format, ws, &y, &yo, &part, &gs, &g3, &t3, &tbuf);
+  fp4_bwd_layout(s, wt.format, ws, &y, &yo, &part, &gs, &g3, &t3, &tbuf, &gbuf);
   const float* t = T_saved;
   if (!t) {
     qlora_status q = lora_down_T(X, A, s, part, tbuf, nullptr, st);
@@ -1375,7 +1391,7 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   QL_MAP(&tb, kBF16, B, s.N, s.r, s.N * 2, 64, 64, kSW128);    // B [r, N] K-major
   QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
-                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, gs, g3, t,
+                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, gbuf, gs, g3, t,
                     t3, dX ? y.gscale : nullptr, dX ? wt.gscale : nullptr, 3));
   QL_MAP(&ga, kBF16, X, s.K, s.M, s.K * 2, 64, 64, kSW128);    // X as MN-major (k inner)
   QL_MAP(&gb, kBF16, g3, 192, s.M, 384, 64, 64, kSW128);       // G in three parts, MN-major
@@ -1392,8 +1408,8 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   }
   qlora_status q = QLORA_OK;
   if (dX) {
-    const Fp4Ext ext{A, gs, s.r, false};
-    q = fp4_product(y, wt, &ext, dX, false, st);
+    const Fp4Ext ext{A, gs, gbuf, 1, nullptr, s.r, s.scale, false};
+    q = fp4_product(y, wt, &ext, dX, false, false, st);
   }
   cudaError_t e = cudaSuccess;
   if (q == QLORA_OK)

@@ -158,16 +158,29 @@ cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int6
                                        const Fp4Out& w, const Fp4Out& wt, void* ws,
                                        cudaStream_t st);
 cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st);
-// The rank-r term added to a product a b^T: sum_j p[j, n] q[m, j] with q as bf16 hi | lo
-// pairs [M, 128], in units of the two gscales; p is [r, N] (mn_major) or [N, r].
+// Few tokens (linear forward): quantizes X [M, K] bf16 to `out` and writes the parts of T = X A
+// over K, fp32 [fp4_prep_parts(K)][M][r], in one launch.
+int fp4_prep_parts(int64_t K);
+cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out& out,
+                            const uint16_t* A, int r, float* T, cudaStream_t st);
+// The rank-r term added to a product a b^T: scale sum_j p[j, n] t[m, j]; p is [r, N]
+// (mn_major) or [N, r]. Above kFp4SplitMaxM tokens it is taken from q, bf16 hi | lo pairs
+// [M, 128] of scale t in units of the two gscales; up to there from t itself, the sum of
+// t_parts arrays [M, r], which is also stored to t_out where that is given.
 struct Fp4Ext {
   const uint16_t* p;
   const uint16_t* q;
+  const float* t;
+  int t_parts;
+  float* t_out;
   int r;
+  float scale;
   bool mn_major;
 };
+constexpr int64_t kFp4SplitMaxM = 128;
+// early: the previous launch on `st` is launch_fp4_prep.
 qlora_status fp4_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
-                         void* out, bool out_f32, cudaStream_t st);
+                         void* out, bool out_f32, bool early, cudaStream_t st);
 // The linear layer on a microscaled weight (gemm.cu): w is W [N, K], wt its transposed copy.
 size_t fp4_fwd_workspace(const LinearShape& s, int format);
 size_t fp4_bwd_workspace(const LinearShape& s, int format);

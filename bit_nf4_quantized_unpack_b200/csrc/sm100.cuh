@@ -351,6 +351,17 @@ __device__ __forceinline__ float ld_cluster_f32(const void* local, uint32_t rank
   return v;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f32x4(const void* local, uint32_t rank) {
+  uint32_t ra;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(ra)
+               : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- CTA pairs (cta_group::2)
 // A cluster of two CTAs works on one tile: one thread of the leader (rank 0) issues the MMAs,
 // which read operands and scales from, and accumulate into, both CTAs' memories at the same
