@@ -472,6 +472,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (rank == 0 && elect_one()) {
       const uint32_t idesc_ext = idesc_bf16_f32(kPairTile, kPairTile, args.ext_mn, false);
       const uint32_t ext_adv = args.ext_mn ? 128u : 2u;
+      // descriptors of slot 0; the start-address field counts 16 bytes
+      const uint64_t dp0 = smem_desc_sw128(smem_u32(p_s), 16, 1024);
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+      const uint64_t dp_ext0 = args.ext_mn ? smem_desc_sw128(smem_u32(p_s), 8192, 1024) : dp0;
+      const uint64_t dsp0 = smem_desc_scales(smem_u32(sfp_s)), dsq0 = smem_desc_scales(smem_u32(sfq_s));
+      // MMAs of a tile's last step: K may end inside it
+      const int tail_mmas = static_cast<int>((args.K - static_cast<int64_t>(args.steps - 1) * kStepCols + 63) / 64);
       int n = 0;
       bool ok = true;
       for (int i = 0; i < my_tiles && ok; ++i) {
@@ -482,42 +489,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         for (int k = 0; k < total && ok; ++k) {
           const int s = n % S;
-          ok = mbar_wait(&full[s], (n / S) & 1u, abort_flag);
           // The scale columns of this step were last read by the MMAs two steps ago (two sets,
           // used in turn), and MMAs of different kinds are not ordered with each other: wait
           // for the completion of step n - 2, or of n - 1 where the kind changes. (At the
           // start of a tile everything before it is complete: its epilogue has begun.)
-          if (ok && k == ext && ext)
-            ok = mbar_wait(&empty[(n - 1) % S], ((n - 1) / S) & 1u, abort_flag);
-          else if (ok && k >= ext + 2)
-            ok = mbar_wait(&empty[(n - 2) % S], ((n - 2) / S) & 1u, abort_flag);
+          const int before = ext && k == ext ? n - 1 : k >= ext + 2 ? n - 2 : -1;
+          ok = before >= 0 ? mbar_wait_both(&full[s], (n / S) & 1u, &empty[before % S],
+                                            (before / S) & 1u, abort_flag)
+                           : mbar_wait(&full[s], (n / S) & 1u, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t pa = smem_u32(p_s + s * kPBytes);
-          const uint64_t dq = smem_desc_sw128(smem_u32(q_s + s * kPairQBytes), 16, 1024);
+          const uint64_t dq = dq0 + static_cast<uint32_t>(s) * (kPairQBytes >> 4);
           if (k < ext) {
-            const uint64_t dp = args.ext_mn ? smem_desc_sw128(pa, 8192, 1024) : smem_desc_sw128(pa, 16, 1024);
+            const uint64_t dp = dp_ext0 + static_cast<uint32_t>(s) * (kPBytes >> 4);
             for (int kk = 0; kk < args.ext_mmas; ++kk)
               umma_bf16_pair(d, dp + kk * ext_adv, dq + kk * 2u, idesc_ext, (k | kk) != 0);
           } else {
-            const uint64_t dp = smem_desc_sw128(pa, 16, 1024);
+            const uint64_t dp = dp0 + static_cast<uint32_t>(s) * (kPBytes >> 4);
+            const uint64_t sp = dsp0 + static_cast<uint32_t>(s) * (kPairSf >> 4);
+            const uint64_t sq = dsq0 + static_cast<uint32_t>(s) * (2 * kPairSf >> 4);
             const uint32_t sfp = tmem + kSfCol + (n & 1) * 48, sfq = sfp + 16;
-            const uint32_t sp = smem_u32(sfp_s + s * kPairSf), sq = smem_u32(sfq_s + s * 2 * kPairSf);
-            const int64_t left = args.K - static_cast<int64_t>(k - ext) * kStepCols;
-            const int mmas = left >= kStepCols ? 4 : static_cast<int>((left + 63) / 64);
+            // scale tile tl and the MMAs that use it
+            auto tile = [&](int tl, int mmas) {
+              tmem_cp_scales_pair(sfp + tl * 4, sp + tl * (kSfTile >> 4));
+              tmem_cp_scales_pair(sfq + tl * 8, sq + tl * (kSfTile >> 4));
+              tmem_cp_scales_pair(sfq + tl * 8 + 4, sq + ((kSfBytes + tl * kSfTile) >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk >= mmas) break;
-              const int tl = kk / kMmaTile, sub = kk % kMmaTile;
-              if (sub == 0) {
-                tmem_cp_scales_pair(sfp + tl * 4, smem_desc_scales(sp + tl * kSfTile));
-                tmem_cp_scales_pair(sfq + tl * 8, smem_desc_scales(sq + tl * kSfTile));
-                tmem_cp_scales_pair(sfq + tl * 8 + 4, smem_desc_scales(sq + kSfBytes + tl * kSfTile));
+              for (int sub = 0; sub < kMmaTile; ++sub) {
+                const int kk = tl * kMmaTile + sub;
+                if (kk < mmas)
+                  umma_fp4_pair<F == Fp4::kMx ? 2 : 4>(
+                      d, dp + kk * 2u, dq + kk * 2u,
+                      idesc_fp4(kPairTile, kPairTile, F == Fp4::kMx, F == Fp4::kMx ? 2 * sub : 0),
+                      sfp + tl * 4, sfq + tl * 8, (k | kk) != 0);
               }
-              umma_fp4_pair<F == Fp4::kMx ? 2 : 4>(
-                  d, dp + kk * 2u, dq + kk * 2u,
-                  idesc_fp4(kPairTile, kPairTile, F == Fp4::kMx, F == Fp4::kMx ? 2 * sub : 0),
-                  sfp + tl * 4, sfq + tl * 8, (k | kk) != 0);
+            };
+            if (k < total - 1 || tail_mmas == 4) {
+#pragma unroll
+              for (int tl = 0; tl < kTileStep; ++tl) tile(tl, 4);
+            } else {
+#pragma unroll
+              for (int tl = 0; tl < kTileStep; ++tl)
+                if (tl * kMmaTile < tail_mmas) tile(tl, tail_mmas);
             }
           }
           umma_commit_pair(&empty[s]);

@@ -85,6 +85,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// Wait for two barriers; their first tests are in flight together (one takes 100 cycles or so).
+__device__ __forceinline__ bool mbar_wait_both(uint64_t* a, uint32_t parity_a, uint64_t* b,
+                                               uint32_t parity_b, volatile int* abort) {
+  const bool ready_a = mbar_try_wait(a, parity_a), ready_b = mbar_try_wait(b, parity_b);
+  if (!ready_a && !mbar_wait(a, parity_a, abort)) return false;
+  return ready_b || mbar_wait(b, parity_b, abort);
+}
+
 // Record the first error code of the launch in the device error word and tell the CTA's
 // other roles to give up their waits.
 __device__ __forceinline__ void record_error(int* err, volatile int* abort, int code) {
