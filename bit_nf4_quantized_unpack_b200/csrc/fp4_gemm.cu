@@ -485,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t d = tmem + (i & 1) * kAcc1;
         // The epilogue has the shared columns of tile i - 1 in registers (and, having begun
         // that tile, all of tile i - 2, which used this accumulator).
-        if (i >= 1) ok = mbar_wait_cluster(acc_part, (i - 1) & 1u, abort_flag);
+        if (i >= 1) ok = mbar_wait(acc_part, (i - 1) & 1u, abort_flag);
         tc_fence_after();
         for (int k = 0; k < total && ok; ++k) {
           const int s = n % S;

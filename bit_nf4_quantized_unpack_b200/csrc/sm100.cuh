@@ -381,32 +381,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t ran
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(rank));
   return ra;
 }
-// Arrive (release at cluster scope) on the mbarrier at a cluster address.
+// Arrive on the mbarrier at a cluster address, without ordering this thread's memory accesses
+// (a release at cluster scope takes 1000 cycles or more): for hand-overs of tensor memory,
+// which tcgen05.wait and the tcgen05 fences order.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// mbar_wait for a barrier that the other CTA's threads arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 63) == 63) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > kWaitTimeoutNs) return false;
-    }
-  }
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // tma_load_2d whose barrier (a cluster address) may be the other CTA's of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* smem_dst, const void* map, uint32_t bar,
