@@ -46,13 +46,10 @@ struct Raw16<true> {
     return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
   }
   __device__ __forceinline__ uint32_t amax() const {
-    uint32_t hi = 0u, lo = 0u;
+    uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi = max(hi, w[i] & kMag);          // the odd value, and bits below it that cannot raise
-      lo = max(lo, w[i] << 16 & kMag);    // it past the next bf16
-    }
-    return max(hi & 0xFFFF0000u, lo);
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);  // two 16-bit maxima
+    return max(m & 0xFFFF0000u, m << 16);
   }
 };
 template <>
@@ -89,12 +86,6 @@ __device__ __forceinline__ uint32_t finite_amax(const R& r) {
     if (b < kInf) m = max(m, b);
   }
   return m;
-}
-
-// The two bf16 values of a word.
-__device__ __forceinline__ void expand2(uint32_t w, float* v) {
-  v[0] = __uint_as_float(w << 16);
-  v[1] = __uint_as_float(w & 0xFFFF0000u);
 }
 
 // x / d for positive normal d, correctly rounded: the reciprocal's product and one correction
@@ -198,65 +189,79 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ NVFP4 rows
-// One CTA per row; the row stays in registers (U chunks a thread) between the row maximum
-// and the codes. U = 0: rows too long for that are read twice.
+// A CTA takes every gridDim.x-th row. The row stays in registers (U chunks a thread) between
+// the row maximum and the codes; with one chunk a thread the next row is fetched meanwhile.
+// U = 0: rows too long for that are read twice.
 template <bool BF16, int U>
 __global__ void __launch_bounds__(512)
-    k_fp4_quantize_nv(const void* __restrict__ X, int64_t cols, uint8_t* __restrict__ codes,
-                      uint8_t* __restrict__ scales, float* __restrict__ gscale) {
+    k_fp4_quantize_nv(const void* __restrict__ X, uint32_t rows, int64_t cols,
+                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                      float* __restrict__ gscale) {
   griddep_wait_and_release();
-  __shared__ uint32_t part[16];
+  __shared__ uint32_t part[2][16];  // warps' maxima, of even and odd passes
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int64_t row = blockIdx.x;
   const int chunks = static_cast<int>(cols / kChunk), padded = (chunks + 3) & ~3;
-  Raw16<BF16> raw[U > 0 ? U : 1];
-  uint32_t top = 0u;
-  auto join = [&](const Raw16<BF16>& r) {
-    uint32_t m = r.amax();
-    if (m >= kInf) m = finite_amax(r);
-    top = max(top, m);
-  };
-  if constexpr (U > 0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (tid + u * nt < chunks) raw[u].load(X, row * cols + static_cast<int64_t>(tid + u * nt) * kChunk);
-      else raw[u].zero();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) join(raw[u]);
-  } else {
-    for (int c = tid; c < chunks; c += nt) {
-      raw[0].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
-      join(raw[0]);
-    }
-  }
-  top = __reduce_max_sync(~0u, top);
-  if ((tid & 31) == 0) part[tid >> 5] = top;
-  __syncthreads();
-  for (int w = 0; w < (nt >> 5); ++w) top = max(top, part[w]);
-  const int e = nv_gscale_exp(top);
-  if (tid == 0) gscale[row] = pow2_f32(e);
-  const float g_inv = pow2_f32(-e);
   const int64_t ktiles = padded / 4;
-  auto emit = [&](int c, const Raw16<BF16>& r) {
-    const bool in = c < chunks;
-    const uint32_t sb = in ? scale_byte<Fp4::kNv>(r.amax(), g_inv) : 0u;
-    if (in)
-      *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<int64_t>(c) * (kChunk / 2)) =
-          codes16<Fp4::kNv>(r, sb, g_inv);
-    const uint32_t w = gather4<Fp4::kNv>(sb);
-    if ((c & 3) == 0 && c < padded)
-      *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, c, ktiles)) = w;
+  Raw16<BF16> raw[U > 0 ? U : 1], next;
+  uint32_t am[U > 0 ? U : 1];
+  auto fetch = [&](int64_t row, int u, Raw16<BF16>& r) {
+    if (row < rows && tid + u * nt < chunks)
+      r.load(X, row * cols + static_cast<int64_t>(tid + u * nt) * kChunk);
+    else
+      r.zero();
   };
-  if constexpr (U > 0) {
+  if constexpr (U == 1) fetch(blockIdx.x, 0, next);
+  int pass = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, pass ^= 1) {
+    uint32_t top = 0u;
+    auto join = [&](const Raw16<BF16>& r) {
+      const uint32_t m = r.amax();
+      top = max(top, m < kInf ? m : finite_amax(r));
+      return m;
+    };
+    if constexpr (U > 0) {
+      if constexpr (U == 1) {
+        raw[0] = next;
+        fetch(row + gridDim.x, 0, next);
+      } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u * nt < padded) emit(tid + u * nt, raw[u]);
-  } else {
-    for (int c = tid; c - tid < padded; c += nt) {
-      if (c < chunks) raw[0].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
-      else raw[0].zero();
-      emit(c, raw[0]);
+        for (int u = 0; u < U; ++u) fetch(row, u, raw[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) am[u] = join(raw[u]);
+    } else {
+      for (int c = tid; c < chunks; c += nt) {
+        raw[0].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
+        join(raw[0]);
+      }
+    }
+    top = __reduce_max_sync(~0u, top);
+    if ((tid & 31) == 0) part[pass][tid >> 5] = top;
+    __syncthreads();  // a warp writes part[pass] again only past the next pass's barrier
+    for (int w = 0; w < (nt >> 5); ++w) top = max(top, part[pass][w]);
+    const int e = nv_gscale_exp(top);
+    if (tid == 0) gscale[row] = pow2_f32(e);
+    const float g_inv = pow2_f32(-e);
+    auto emit = [&](int c, const Raw16<BF16>& r, uint32_t m) {
+      const bool in = c < chunks;
+      const uint32_t sb = in ? scale_byte<Fp4::kNv>(m, g_inv) : 0u;
+      if (in)
+        *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<int64_t>(c) * (kChunk / 2)) =
+            codes16<Fp4::kNv>(r, sb, g_inv);
+      const uint32_t w = gather4<Fp4::kNv>(sb);
+      if ((c & 3) == 0 && c < padded)
+        *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, c, ktiles)) = w;
+    };
+    if constexpr (U > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u * nt < padded) emit(tid + u * nt, raw[u], am[u]);
+    } else {
+      for (int c = tid; c - tid < padded; c += nt) {
+        if (c < chunks) raw[0].load(X, row * cols + static_cast<int64_t>(c) * kChunk);
+        else raw[0].zero();
+        emit(c, raw[0], raw[0].amax());
+      }
     }
   }
 }
@@ -432,31 +437,37 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
 static_assert(kPrepTok * kPrepCols == kPrepThreads && 8 * 256 * 4 <= kPrepTok * kPrepXPitch, "sums");
 
 // ------------------------------------------------------------------ weights, square blocks
-// Largest finite magnitude of the matrix, as fp32 bits in *top (zero before the launch).
+constexpr int kAmaxChunks = 4;  // per thread, all in flight
+// Largest finite magnitude of the matrix, as fp32 bits in *top (zero before the launch). One
+// atomic per CTA: one per warp on the single address took longer than the reading.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     k_fp4_amax(const void* __restrict__ W, int64_t chunks, uint32_t* __restrict__ top) {
   griddep_wait_and_release();
-  constexpr int U = BF16 ? 4 : 2;  // chunks in flight per thread
+  __shared__ uint32_t part[8];
   uint32_t m = 0u;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; c < chunks;
-       c += stride * U) {
-    Raw16<BF16> r[U];
+  constexpr int64_t kBatch = 256 * kAmaxChunks;
+  for (int64_t c0 = blockIdx.x * kBatch + threadIdx.x; c0 < chunks; c0 += gridDim.x * kBatch) {
+    Raw16<BF16> r[kAmaxChunks];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (c + u * stride < chunks) r[u].load(W, (c + u * stride) * kChunk);
+    for (int u = 0; u < kAmaxChunks; ++u) {
+      if (c0 + u * 256 < chunks) r[u].load(W, (c0 + u * 256) * kChunk);
       else r[u].zero();
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t a = r[u].amax();
-      if (a >= kInf) a = finite_amax(r[u]);
-      m = max(m, a);
+    for (int u = 0; u < kAmaxChunks; ++u) {
+      const uint32_t a = r[u].amax();
+      m = max(m, a < kInf ? a : finite_amax(r[u]));
     }
   }
   m = __reduce_max_sync(~0u, m);
-  if ((threadIdx.x & 31) == 0 && m) atomicMax(top, m);  // a maximum: no order to depend on
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) m = max(m, part[w]);
+    if (m) atomicMax(top, m);  // a maximum: no order to depend on
+  }
 }
 
 // Transpose of an 8 x 8 square of nibbles, one word per row: swaps 4 x 4, 2 x 2 and single
@@ -475,12 +486,13 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
   }
 }
 
+constexpr int kWeightWarps = 4;  // of a CTA; eight were 7 % slower
 // A warp takes 32 rows x 64 columns of W, a lane 8 x 8 of it (lane = row group * 8 + column
 // group), so that squares of 16 and of 32 are whole in the warp: the maxima go through
 // shuffles, the transposed codes through an 8 x 8 nibble transpose in registers. The
 // transposed copy has the same squares, so it stores the same values.
 template <Fp4 F, bool BF16>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kWeightWarps)
     k_fp4_quantize_weight(const void* __restrict__ W, int64_t n, int64_t k,
                           const uint32_t* __restrict__ top, uint8_t* __restrict__ codes,
                           uint8_t* __restrict__ scales, float* __restrict__ gscale,
@@ -488,7 +500,7 @@ __global__ void __launch_bounds__(256)
   griddep_wait_and_release();
   constexpr int B = kFp4Block<F>;
   const int lane = threadIdx.x & 31, kl = lane & 7, nl = lane >> 3;
-  const int64_t k0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 64;
+  const int64_t k0 = (static_cast<int64_t>(blockIdx.x) * kWeightWarps + (threadIdx.x >> 5)) * 64;
   const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 32;
   if (k0 >= k) return;
   float g_inv = 1.f;
@@ -526,10 +538,19 @@ __global__ void __launch_bounds__(256)
       return (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
     }
   };
+  if constexpr (BF16) {
+    constexpr uint32_t kMag2 = 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i)
+      am = __vmaxu2(am, __vmaxu2(__vmaxu2(rb[i].x & kMag2, rb[i].y & kMag2),
+                                 __vmaxu2(rb[i].z & kMag2, rb[i].w & kMag2)));
+    am = max(am & 0xFFFF0000u, am << 16);
+  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(at(i, j)) & kMag);
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(at(i, j)) & kMag);
+  }
   am = max(am, __shfl_xor_sync(~0u, am, 1));
   am = max(am, __shfl_xor_sync(~0u, am, 8));
   if (F == Fp4::kMx) {
@@ -664,26 +685,32 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
               : u == 2 ? k_fp4_quantize_nv<BF16, 2>
               : u == 4 ? k_fp4_quantize_nv<BF16, BF16 ? 4 : 0>
                        : k_fp4_quantize_nv<BF16, 0>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, st, X, cols, codes,
-                    scales, gscale);
+  // as many CTAs as run at one time
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * std::max(per_sm, 1));
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, st, X,
+                    static_cast<uint32_t>(rows), cols, codes, scales, gscale);
 }
 
 template <bool BF16>
 cudaError_t quantize_weight(const void* W, int64_t n, int64_t k, int format, const Fp4Out& w,
                             const Fp4Out& wt, uint32_t* top, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((k + 511) / 512), static_cast<unsigned>(n / 32));
+  const dim3 grid(static_cast<unsigned>((k + 64 * kWeightWarps - 1) / (64 * kWeightWarps)), static_cast<unsigned>(n / 32));
   if (format == QLORA_FP4_MX)
-    return launch_pdl(k_fp4_quantize_weight<Fp4::kMx, BF16>, grid, dim3(256), 0, st, W, n, k,
+    return launch_pdl(k_fp4_quantize_weight<Fp4::kMx, BF16>, grid, dim3(32 * kWeightWarps), 0, st, W, n, k,
                       static_cast<const uint32_t*>(nullptr), w.codes, w.scales, w.gscale, wt.codes,
                       wt.scales);
   cudaError_t e = cudaMemsetAsync(top, 0, sizeof(uint32_t), st);
   if (e != cudaSuccess) return e;
   const int64_t chunks = n * k / kChunk;
-  const int64_t blocks = std::min<int64_t>((chunks + 255) / 256, static_cast<int64_t>(num_sms()) * 8);
+  const int64_t blocks = std::min<int64_t>((chunks + 256 * kAmaxChunks - 1) / (256 * kAmaxChunks),
+                                           static_cast<int64_t>(num_sms()) * 8);
   e = launch_pdl(k_fp4_amax<BF16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, W, chunks,
                  top);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_fp4_quantize_weight<Fp4::kNv, BF16>, grid, dim3(256), 0, st, W, n, k,
+  return launch_pdl(k_fp4_quantize_weight<Fp4::kNv, BF16>, grid, dim3(32 * kWeightWarps), 0, st, W, n, k,
                     static_cast<const uint32_t*>(top), w.codes, w.scales, w.gscale, wt.codes,
                     wt.scales);
 }

@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
   griddep_wait_and_release();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int issued = 0;
       for (int i = 0; i < nsteps; ++i) {
         const int s = i % kLoraStages;
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
           mbar_wait_drain(&full[i % kLoraStages], (i / kLoraStages) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, NC, A_MN, B_MN);
       bool ok = true;
       for (int i = 0; i < nsteps; ++i) {
