@@ -1,5 +1,8 @@
 """Build the C-ABI library ``lib/libqlora.so`` from ``csrc/`` with nvcc for sm_100a.
 
+The Python calls of the microscaled 4-bit operators go through a second, small library,
+``lib/qlora_binding.so`` (g++, torch's headers), which loads the first.
+
 Run ``python -m bit_nf4_quantized_unpack_b200.build`` (or call ``build()``). Objects go
 to ``_build/`` at the repository root; the library is written in-tree next to this
 file so that it ships with a snapshot of the repository.
@@ -17,6 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "lib", "libqlora.so")
+BINDING_SRC = os.path.join(CSRC, "binding", "fp4_binding.cpp")
+BINDING = os.path.join(PKG, "lib", "qlora_binding.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -37,7 +42,7 @@ def sources():
 
 
 def _deps_mtime():
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "qlora.h"), __file__]
+    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if "." in f] + [os.path.join(INCLUDE, "qlora.h"), __file__]
     return max(os.path.getmtime(p) for p in paths)
 
 
@@ -55,9 +60,44 @@ def _compile(src, verbose):
     return obj, res.stderr if verbose else ""
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the Python binding against the running interpreter's torch."""
+    newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "qlora.h"), __file__))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    includes = [os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                cuda_inc, sysconfig.get_paths()["include"]]
+    os.makedirs(os.path.dirname(BINDING), exist_ok=True)
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for i in includes for a in ("-isystem", i)], BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+           "-ltorch_python", "-ldl"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA/C++ source for sm_100a and link the shared library.
-    Returns the library path. Skips work when the library is newer than its sources."""
+    """Compile every CUDA/C++ source for sm_100a and link the shared library, and the Python
+    binding. Returns the library path. Skips what is newer than its sources."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(build_binding, force)
+        path = _build_library(force, verbose)
+        binding.result()
+    return path
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB
     os.makedirs(OBJ, exist_ok=True)

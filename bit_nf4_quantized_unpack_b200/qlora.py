@@ -472,19 +472,34 @@ def qlora_adamw_step(p: torch.Tensor, g: torch.Tensor, state, step: int, *, lr: 
 
 
 # ------------------------------------------- microscaled 4-bit floating point (MXFP4, NVFP4)
-# A decode step makes several of these calls per linear, and at a few tokens the host is what
-# bounds them: the checks below read only cheap tensor attributes, and the raw stream handle
-# (0.1 us) takes the place of a Stream object (3.2 us).
+# Checks, allocation and marshalling of these calls are in C++ (csrc/binding): a decode step
+# makes several per linear, and at a few tokens the host is what bounds them.
 FP4_MXFP4, FP4_NVFP4 = 0, 1
-_FP4_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
-_U8, _BF, _FL = torch.uint8, torch.bfloat16, torch.float32
-_empty = torch.empty
+BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "qlora_binding.so")
+_binding = None
 
 
-def _fp4_scales_bytes(rows: int, cols: int, fmt: int) -> int:
-    """qlora_fp4_scales_bytes without the call: tiles of 128 rows x 4 blocks of 512 bytes."""
-    per = 128 if fmt == FP4_MXFP4 else 64
-    return (rows + 127) // 128 * ((cols + per - 1) // per) * 512
+def binding():
+    """The loaded C++ binding (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -m bit_nf4_quantized_unpack_b200.build`")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("qlora_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.open(LIB_PATH, QLoraError)
+        _binding = module
+    return _binding
+
+
+def _bf16(dtype: torch.dtype) -> bool:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}")
+    return dtype is torch.bfloat16
 
 
 @dataclass
@@ -497,22 +512,18 @@ class FP4Matrix:
     cols: int
     fmt: int = FP4_NVFP4
 
-    def c_struct(self) -> CFP4Matrix:
-        g = self.gscale
-        return CFP4Matrix(self.codes.data_ptr(), self.scales.data_ptr(),
-                          None if g is None else g.data_ptr(), 0 if g is None else g.numel(),
-                          self.rows, self.cols, self.fmt)
-
     @staticmethod
     def empty(rows: int, cols: int, fmt: int = FP4_NVFP4, device="cuda",
               gscale_rows: int | None = None) -> "FP4Matrix":
         """Uninitialised storage; gscale_rows: rows (default) or 1, NVFP4 only."""
-        if rows < 0 or cols < 32 or cols % 32 or fmt not in (FP4_MXFP4, FP4_NVFP4):
+        nsc = int(lib().qlora_fp4_scales_bytes(rows, cols, fmt))
+        if nsc == 0 and rows != 0:
             raise QLoraError(2, "FP4Matrix", f"[{rows}, {cols}], format {fmt}")
-        return FP4Matrix(_empty((rows, cols // 2), dtype=_U8, device=device),
-                         _empty(_fp4_scales_bytes(rows, cols, fmt), dtype=_U8, device=device),
-                         _empty(rows if gscale_rows is None else gscale_rows, dtype=_FL,
-                                device=device) if fmt == FP4_NVFP4 else None, rows, cols, fmt)
+        ng = rows if gscale_rows is None else gscale_rows
+        return FP4Matrix(torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
+                         torch.empty(nsc, dtype=torch.uint8, device=device),
+                         torch.empty(ng, dtype=torch.float32, device=device)
+                         if fmt == FP4_NVFP4 else None, rows, cols, fmt)
 
 
 @dataclass
@@ -522,79 +533,18 @@ class FP4Weight:
     wt: FP4Matrix | None = None
 
 
-def _fp4_in(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
-    """The address of a dense CUDA tensor on device `dev` with this dtype and shape."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, "
-                         f"got {tuple(t.shape)} with strides {t.stride()}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
-    return t.data_ptr()
-
-
-def _fp4_device(t: torch.Tensor, name: str) -> int:
-    """The device index of the operand that the others have to share."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    return t.get_device()
-
-
-def _fp4_matrix(q: FP4Matrix, name: str, dev: int) -> CFP4Matrix:
-    """The C form, after checking that the buffers hold what the sizes say (no kernel reads
-    past them)."""
-    rows, cols, g = q.rows, q.cols, q.gscale
-    return CFP4Matrix(
-        _fp4_in(q.codes, name + ".codes", dev, _U8, (rows, cols // 2)),
-        _fp4_in(q.scales, name + ".scales", dev, _U8, (_fp4_scales_bytes(rows, cols, q.fmt),)),
-        None if g is None else _fp4_in(g, name + ".gscale", dev, _FL, (rows,) if g.numel() != 1 else (1,)),
-        0 if g is None else g.numel(), rows, cols, q.fmt)
-
-
-def _fp4_workspace(workspace, need: int, dev: int, device):
-    """A byte buffer of at least `need` bytes (the library checks a caller's size)."""
-    if workspace is None:
-        return _empty(need if need > 16 else 16, dtype=_U8, device=device)
-    _fp4_in(workspace, "workspace", dev, _U8, workspace.shape)
-    return workspace
-
-
-def _fp4_call(name: str, dev: int, *args) -> None:
-    """One C call on the operands' device and its current stream."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            status = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        status = getattr(_lib, name)(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if status:
-        _check(status, name)
-
-
 def qlora_fp4_quantize(X: torch.Tensor, fmt: int = FP4_NVFP4,
                        out: FP4Matrix | None = None) -> FP4Matrix:
     """X [rows, cols] (fp32 or bf16, CUDA, contiguous) to microscaled form, each row by
     itself; cols % 32 == 0."""
-    lib()
-    dtype = _FP4_DTYPES.get(X.dtype)
-    if dtype is None:
-        raise TypeError(f"X: unsupported dtype {X.dtype}")
-    dev = _fp4_device(X, "X")
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D")
-    rows, cols = X.shape
-    x = _fp4_in(X, "X", dev, X.dtype, X.shape)
+    ext = _binding or binding()
     if out is None:
-        q = FP4Matrix.empty(rows, cols, fmt, X.device)
-        _fp4_call("qlora_fp4_quantize", dev, x, dtype, rows, cols, fmt, q.codes.data_ptr(),
-                  q.scales.data_ptr(), None if q.gscale is None else q.gscale.data_ptr())
-        return q
-    if (out.rows, out.cols, out.fmt) != (rows, cols, fmt):
+        c, s, g = ext.quantize(X, fmt)
+        rows, cols = X.shape
+        return FP4Matrix(c, s, g, rows, cols, fmt)
+    if (out.rows, out.cols, out.fmt) != (*X.shape, fmt):
         raise ValueError("out: another shape or format than X")
-    c = _fp4_matrix(out, "out", dev)
-    if fmt == FP4_NVFP4 and c.gscale_rows != rows:
-        raise ValueError("out.gscale: expected one value per row")
-    _fp4_call("qlora_fp4_quantize", dev, x, dtype, rows, cols, fmt, c.codes, c.scales, c.gscale)
+    ext.quantize_out(X, fmt, out.codes, out.scales, out.gscale)
     return out
 
 
@@ -603,72 +553,37 @@ def qlora_fp4_quantize_weight(W: torch.Tensor, fmt: int = FP4_NVFP4, transposed:
                               workspace: torch.Tensor | None = None) -> FP4Weight:
     """W [n_out, k_in] (fp32 or bf16, CUDA, contiguous, multiples of 32) with square blocks;
     transposed: also the copy that the backward reads (w and wt share one gscale)."""
-    lib()
-    dtype = _FP4_DTYPES.get(W.dtype)
-    if dtype is None:
-        raise TypeError(f"W: unsupported dtype {W.dtype}")
-    dev = _fp4_device(W, "W")
-    if W.dim() != 2:
-        raise ValueError("W must be 2-D")
-    n, k = W.shape
-    src = _fp4_in(W, "W", dev, W.dtype, W.shape)
+    ext = _binding or binding()
     if out is None:
-        w, wt = FP4Matrix.empty(n, k, fmt, W.device, gscale_rows=1), None
-        if transposed:
-            if n < 32 or n % 32:
-                raise QLoraError(2, "qlora_fp4_quantize_weight", f"[{n}, {k}]")
-            wt = FP4Matrix(_empty((k, n // 2), dtype=_U8, device=W.device),
-                           _empty(_fp4_scales_bytes(k, n, fmt), dtype=_U8, device=W.device),
-                           w.gscale, k, n, fmt)
-    else:
-        w, wt = out.w, out.wt if transposed else None
-        if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
-                wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):
-            raise ValueError("out: another shape or format than W")
-        if fmt == FP4_NVFP4 and (w.gscale is None or w.gscale.numel() != 1):
-            raise ValueError("out.w.gscale: expected one value")
-    c = _fp4_matrix(w, "out.w", dev)
-    tc = ts = None
+        c, s, g, tc, ts = ext.weight(W, fmt, transposed, workspace)
+        n, k = W.shape
+        return FP4Weight(FP4Matrix(c, s, g, n, k, fmt),
+                         FP4Matrix(tc, ts, g, k, n, fmt) if transposed else None)
+    w, wt = out.w, out.wt if transposed else None
+    n, k = W.shape
+    if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
+            wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):
+        raise ValueError("out: another shape or format than W")
+    ext.weight_out(W, fmt, w.codes, w.scales, w.gscale, wt.codes if wt else None,
+                   wt.scales if wt else None, workspace)
     if wt is not None:
         wt.gscale = w.gscale
-        t = _fp4_matrix(wt, "out.wt", dev)
-        tc, ts = t.codes, t.scales
-    ws = _fp4_workspace(workspace, _lib.qlora_fp4_quantize_weight_workspace_size(), dev, W.device)
-    _fp4_call("qlora_fp4_quantize_weight", dev, src, dtype, n, k, fmt, c.codes, c.scales, c.gscale,
-              tc, ts, ws.data_ptr(), ws.numel())
     return FP4Weight(w, wt)
 
 
 def qlora_fp4_dequant(q: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
                       out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of a microscaled matrix [rows, cols], bf16 or fp32."""
-    lib()
-    dev = _fp4_device(q.codes, "q.codes")
-    c = _fp4_matrix(q, "q", dev)
-    if out is None:
-        out = _empty((q.rows, q.cols), dtype=dtype, device=q.codes.device)
-    code = _FP4_DTYPES.get(out.dtype)
-    if code is None:
-        raise TypeError(f"out: unsupported dtype {out.dtype}")
-    o = _fp4_in(out, "out", dev, out.dtype, (q.rows, q.cols))
-    _fp4_call("qlora_fp4_dequant", dev, c, code, o)
-    return out
+    return (_binding or binding()).dequant(q.codes, q.scales, q.gscale, q.rows, q.cols, q.fmt,
+                                           _bf16(dtype), out)
 
 
 def qlora_fp4_matmul(a: FP4Matrix, b: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
                      out: torch.Tensor | None = None) -> torch.Tensor:
     """a b^T [a.rows, b.rows], bf16 or fp32; both operands of one format, b.rows % 8 == 0."""
-    lib()
-    dev = _fp4_device(a.codes, "a.codes")
-    ca, cb = _fp4_matrix(a, "a", dev), _fp4_matrix(b, "b", dev)
-    if out is None:
-        out = _empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
-    code = _FP4_DTYPES.get(out.dtype)
-    if code is None:
-        raise TypeError(f"out: unsupported dtype {out.dtype}")
-    o = _fp4_in(out, "out", dev, out.dtype, (a.rows, b.rows))
-    _fp4_call("qlora_fp4_matmul", dev, ca, cb, code, o)
-    return out
+    return (_binding or binding()).matmul(a.codes, a.scales, a.gscale, a.rows, a.cols, a.fmt,
+                                          b.codes, b.scales, b.gscale, b.rows, b.cols, b.fmt,
+                                          _bf16(dtype), out)
 
 
 def qlora_fp4_linear_fwd_workspace_size(M: int, n_out: int, k_in: int, r: int,
@@ -686,23 +601,9 @@ def qlora_fp4_linear_fwd(X: torch.Tensor, w: FP4Weight, A: torch.Tensor, B: torc
                          T: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Y = bf16(q(X) W^T + scale (X A) B) on a microscaled weight. Returns (Y, T) with
     T = X A (fp32) or None."""
-    lib()
-    dev, q = _fp4_device(X, "X"), w.w
-    c = _fp4_matrix(q, "w", dev)
-    M, r, n, k, device = X.shape[0], A.shape[1], q.rows, q.cols, X.device
-    x, a = _fp4_in(X, "X", dev, _BF, (M, k)), _fp4_in(A, "A", dev, _BF, (k, r))
-    b = _fp4_in(B, "B", dev, _BF, (r, n))
-    if Y is None:
-        Y = _empty((M, n), dtype=_BF, device=device)
-    y, t = _fp4_in(Y, "Y", dev, _BF, (M, n)), None
-    if save_T:
-        if T is None:
-            T = _empty((M, r), dtype=_FL, device=device)
-        t = _fp4_in(T, "T", dev, _FL, (M, r))
-    ws = _fp4_workspace(workspace, _lib.qlora_fp4_linear_fwd_workspace_size(M, n, k, r, q.fmt), dev,
-                        device)
-    _fp4_call("qlora_fp4_linear_fwd", dev, x, M, c, a, b, r, scale, y, t, ws.data_ptr(), ws.numel())
-    return Y, (T if save_T else None)
+    q = w.w
+    return (_binding or binding()).linear_fwd(X, q.codes, q.scales, q.gscale, q.rows, q.cols, q.fmt,
+                                              A, B, scale, save_T, Y, T, workspace)
 
 
 def qlora_fp4_linear_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor | None, w: FP4Weight,
@@ -711,28 +612,8 @@ def qlora_fp4_linear_bwd(dY: torch.Tensor, X: torch.Tensor, T: torch.Tensor | No
                          dB: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Gradients (dX bf16 or None, dA fp32 [K, r], dB fp32 [r, N]) of qlora_fp4_linear_fwd;
     W is frozen and needs its transposed copy."""
-    lib()
     q = w.wt
     if q is None:
         raise ValueError("w.wt: the backward reads the transposed copy")
-    dev = _fp4_device(X, "X")
-    c = _fp4_matrix(q, "w.wt", dev)
-    M, r, n, k, device = X.shape[0], A.shape[1], q.cols, q.rows, X.device
-    dy, x = _fp4_in(dY, "dY", dev, _BF, (M, n)), _fp4_in(X, "X", dev, _BF, (M, k))
-    a, b = _fp4_in(A, "A", dev, _BF, (k, r)), _fp4_in(B, "B", dev, _BF, (r, n))
-    t = None if T is None else _fp4_in(T, "T", dev, _FL, (M, r))
-    dx = None
-    if need_dX:
-        if dX is None:
-            dX = _empty((M, k), dtype=_BF, device=device)
-        dx = _fp4_in(dX, "dX", dev, _BF, (M, k))
-    if dA is None:
-        dA = _empty((k, r), dtype=_FL, device=device)
-    if dB is None:
-        dB = _empty((r, n), dtype=_FL, device=device)
-    da, db = _fp4_in(dA, "dA", dev, _FL, (k, r)), _fp4_in(dB, "dB", dev, _FL, (r, n))
-    ws = _fp4_workspace(workspace, _lib.qlora_fp4_linear_bwd_workspace_size(M, n, k, r, q.fmt), dev,
-                        device)
-    _fp4_call("qlora_fp4_linear_bwd", dev, dy, x, t, M, c, a, b, r, scale, dx, da, db,
-              ws.data_ptr(), ws.numel())
-    return (dX if need_dX else None), dA, dB
+    return (_binding or binding()).linear_bwd(dY, X, T, q.codes, q.scales, q.gscale, q.rows, q.cols,
+                                              q.fmt, A, B, scale, need_dX, dX, dA, dB, workspace)
