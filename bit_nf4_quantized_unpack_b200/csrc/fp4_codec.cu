@@ -329,13 +329,14 @@ __device__ __forceinline__ void quantize_row(const uint16_t* __restrict__ X, int
   }
 }
 
-// ------------------------------------------------------------------ few tokens: X and T = X A
+// ------------------------------------------------------------------ few tokens: rows and rank-r product
 // One launch for what a few tokens need before their product with the weight, in clusters of
-// eight CTAs. The first ceil(M / 8) clusters quantize one row per CTA. The others take 16
-// tokens, 16 columns of A and 4096 rows of it (512 per CTA, 64 per warp, fetched at once:
-// the time is two memory latencies), multiply with mma.sync, and add up warps and then CTAs
-// in a fixed order, the CTAs through distributed shared memory. The product kernel adds the
-// parts of K above 4096.
+// eight CTAs: X [M, K] in microscaled form, and T = X A with A [K, r] (A_T: stored as [r, K],
+// the backward's G = dY B^T). The first ceil(M / 8) clusters quantize one row per CTA. The
+// others take 16 tokens, 16 columns of A and 4096 rows of it (512 per CTA, 64 per warp,
+// fetched at once: the time is two memory latencies), multiply with mma.sync, and add up
+// warps and then CTAs in a fixed order, the CTAs through distributed shared memory. Who reads
+// T adds the parts of K above 4096.
 constexpr int kPrepThreads = 256;
 constexpr int kPrepTok = 16, kPrepCols = 16;
 constexpr int kPrepSlice = 512;                    // rows of A per CTA
@@ -365,19 +366,18 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <Fp4 F>
+template <Fp4 F, bool A_T>
 __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
     k_fp4_prep(const uint16_t* __restrict__ X, int M, int64_t K, uint8_t* __restrict__ codes,
-               uint8_t* __restrict__ scales, float* __restrict__ gscale,
+               uint8_t* __restrict__ scales, float* __restrict__ gscale, int row_ctas,
                const uint16_t* __restrict__ A, int r, float* __restrict__ T) {
   griddep_wait_and_release();
   __shared__ uint32_t part[16];
   __shared__ __align__(16) uint8_t xs[kPrepTok * kPrepXPitch];
-  __shared__ __align__(16) uint8_t as[kPrepSlice * kPrepAPitch];
+  __shared__ __align__(16) uint8_t as[A_T ? kPrepCols * kPrepXPitch : kPrepSlice * kPrepAPitch];
   __shared__ float mine[kPrepTok * kPrepCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row_ctas = (M + 7) / 8 * 8;
-  if (static_cast<int>(blockIdx.x) < row_ctas) {
+  if (static_cast<int>(blockIdx.x) < row_ctas) {  // whole clusters, or none
     if (static_cast<int>(blockIdx.x) < M)
       quantize_row<F>(X, blockIdx.x, K, codes, scales, gscale, part);
     return;  // the whole cluster takes this branch: its barrier is not used
@@ -389,10 +389,17 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
   const int64_t k0 = (static_cast<int64_t>(kpart) * 8 + rank) * kPrepSlice;
   const uint32_t xs_s = smem_u32(xs), as_s = smem_u32(as);
 #pragma unroll
-  for (int u = 0; u < kPrepSlice * 2 / kPrepThreads; ++u) {  // A: two 16-byte pieces a row
-    const int i = tid + u * kPrepThreads, k = i >> 1, j = (i & 1) * 8;
-    const bool in = k0 + k < K && j0 + j < r;
-    cp_async16(as_s + k * kPrepAPitch + j * 2, in ? A + (k0 + k) * r + j0 + j : A, in);
+  for (int u = 0; u < kPrepSlice * kPrepCols / 8 / kPrepThreads; ++u) {
+    const int i = tid + u * kPrepThreads;
+    if (A_T) {  // 16 rows of 512 columns
+      const int j = i / (kPrepSlice / 8), k = i % (kPrepSlice / 8) * 8;
+      const bool in = k0 + k < K && j0 + j < r;
+      cp_async16(as_s + j * kPrepXPitch + k * 2, in ? A + (j0 + j) * K + k0 + k : A, in);
+    } else {    // 512 rows of 16 columns
+      const int k = i >> 1, j = (i & 1) * 8;
+      const bool in = k0 + k < K && j0 + j < r;
+      cp_async16(as_s + k * kPrepAPitch + j * 2, in ? A + (k0 + k) * r + j0 + j : A, in);
+    }
   }
 #pragma unroll
   for (int u = 0; u < kPrepTok * kPrepSlice / 8 / kPrepThreads; ++u) {
@@ -408,7 +415,10 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
     const int k = warp * (kPrepSlice / 8) + i * 16;
     uint32_t a[4], b[4];
     ldmatrix_x4(xs_s + (lane & 15) * kPrepXPitch + (k + (lane >> 4) * 8) * 2, a);
-    ldmatrix_x4_trans(as_s + (k + (lane & 15)) * kPrepAPitch + (lane >> 4) * 16, b);
+    if (A_T)  // matrices: (columns 0-7, k 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+      ldmatrix_x4(as_s + ((lane & 7) + (lane >> 4) * 8) * kPrepXPitch + (k + ((lane >> 3) & 1) * 8) * 2, b);
+    else
+      ldmatrix_x4_trans(as_s + (k + (lane & 15)) * kPrepAPitch + (lane >> 4) * 16, b);
     mma_16816(acc[0], a, b[0], b[1]);
     mma_16816(acc[1], a, b[2], b[3]);
   }
@@ -435,6 +445,80 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
   cluster_sync_all();  // no CTA leaves while its sums are being read
 }
 static_assert(kPrepTok * kPrepCols == kPrepThreads && 8 * 256 * 4 <= kPrepTok * kPrepXPitch, "sums");
+
+// Few tokens: dA [K, r] = scale X^T G and dB [r, N] = scale T^T dY, G and T fp32 in parts
+// [parts][M][r]. A CTA takes 64 columns of X (or of dY) and all of the rank; a thread 4 x 4
+// outputs, tokens in order, in fp32. For up to 128 tokens this is a few microseconds of FMAs
+// and reads X and dY once; the tensor-core path needs two launches and splits G and T in parts.
+constexpr int kGradCols = 64, kGradTok = 32;
+__global__ void __launch_bounds__(256)
+    k_fp4_small_grads(const uint16_t* __restrict__ X, const uint16_t* __restrict__ dY, int M, int64_t K,
+                      int64_t N, const float* __restrict__ G, int g_parts, const float* __restrict__ T,
+                      int t_parts, int r, float scale, float* __restrict__ dA, float* __restrict__ dB) {
+  griddep_wait_and_release();
+  __shared__ __align__(16) float xs[kGradTok][kGradCols], vs[kGradTok][64];
+  const int tid = threadIdx.x;
+  const int64_t k_ctas = (K + kGradCols - 1) / kGradCols;
+  const bool second = blockIdx.x >= k_ctas;
+  const int64_t C = second ? N : K, c0 = (blockIdx.x - (second ? k_ctas : 0)) * kGradCols;
+  const uint16_t* src = second ? dY : X;
+  const float* val = second ? T : G;
+  const int parts = second ? t_parts : g_parts;
+  const int a4 = (tid & 15) * 4, j4 = (tid >> 4) * 4;
+  float acc[4][4] = {};
+  for (int m0 = 0; m0 < M; m0 += kGradTok) {
+    const int len = min(kGradTok, M - m0);
+    __syncthreads();
+    {
+      const int t = tid >> 3, c = (tid & 7) * 8;  // 32 tokens x 8 groups of 8 columns
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (t < len && c0 + c < C) w = __ldg(reinterpret_cast<const uint4*>(src + (m0 + t) * C + c0 + c));
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xs[t][c + 2 * i] = __uint_as_float(ww[i] << 16);
+        xs[t][c + 2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = c + 4 * h;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < len && j < r)
+          for (int p = 0; p < parts; ++p) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(
+                val + (static_cast<int64_t>(p) * M + m0 + t) * r + j));
+            v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+          }
+        *reinterpret_cast<float4*>(&vs[t][j]) = v;
+      }
+    }
+    __syncthreads();
+    if (j4 < r) {
+#pragma unroll 8
+      for (int t = 0; t < len; ++t) {
+        const float4 x = *reinterpret_cast<const float4*>(&xs[t][a4]);
+        const float4 v = *reinterpret_cast<const float4*>(&vs[t][j4]);
+        const float xa[4] = {x.x, x.y, x.z, x.w}, va[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xa[i], va[j], acc[i][j]);
+      }
+    }
+  }
+  if (j4 >= r || c0 + a4 >= C) return;  // C is a multiple of 32, r of 8
+  if (!second) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(dA + (c0 + a4 + i) * r + j4) =
+          make_float4(scale * acc[i][0], scale * acc[i][1], scale * acc[i][2], scale * acc[i][3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(dB + (j4 + j) * N + c0 + a4) =
+          make_float4(scale * acc[0][j], scale * acc[1][j], scale * acc[2][j], scale * acc[3][j]);
+  }
+}
 
 // ------------------------------------------------------------------ weights, square blocks
 constexpr int kAmaxChunks = 4;  // per thread, all in flight
@@ -738,14 +822,23 @@ cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int6
 
 int fp4_prep_parts(int64_t K) { return static_cast<int>((K + 8 * kPrepSlice - 1) / (8 * kPrepSlice)); }
 
-cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out& out,
-                            const uint16_t* A, int r, float* T, cudaStream_t st) {
-  const int m = static_cast<int>(M);
+cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out* out,
+                            const uint16_t* A, bool a_t, int r, float* T, cudaStream_t st) {
+  const int m = static_cast<int>(M), row_ctas = out ? (m + 7) / 8 * 8 : 0;
   const int jobs = (m + kPrepTok - 1) / kPrepTok * ((r + kPrepCols - 1) / kPrepCols) * fp4_prep_parts(K);
-  const dim3 grid((m + 7) / 8 * 8 + 8 * jobs);
-  auto kern = format == QLORA_FP4_MX ? k_fp4_prep<Fp4::kMx> : k_fp4_prep<Fp4::kNv>;
-  return launch_pdl(kern, grid, dim3(kPrepThreads), 0, st, X, m, K, out.codes, out.scales, out.gscale,
-                    A, r, T);
+  auto kern = format == QLORA_FP4_MX ? (a_t ? k_fp4_prep<Fp4::kMx, true> : k_fp4_prep<Fp4::kMx, false>)
+                                     : (a_t ? k_fp4_prep<Fp4::kNv, true> : k_fp4_prep<Fp4::kNv, false>);
+  const Fp4Out o = out ? *out : Fp4Out{};
+  return launch_pdl(kern, dim3(row_ctas + 8 * jobs), dim3(kPrepThreads), 0, st, X, m, K, o.codes,
+                    o.scales, o.gscale, row_ctas, A, r, T);
+}
+
+cudaError_t launch_fp4_small_grads(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, int64_t N,
+                                   const float* G, int g_parts, const float* T, int t_parts, int r,
+                                   float scale, float* dA, float* dB, cudaStream_t st) {
+  const int64_t ctas = (K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols;
+  return launch_pdl(k_fp4_small_grads, dim3(static_cast<unsigned>(ctas)), dim3(256), 0, st, X, dY,
+                    static_cast<int>(M), K, N, G, g_parts, T, t_parts, r, scale, dA, dB);
 }
 
 cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st) {

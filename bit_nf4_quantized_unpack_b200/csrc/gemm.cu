@@ -1313,21 +1313,47 @@ size_t fp4_fwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matr
   return c.off + 256;
 }
 
-size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, qlora_fp4_matrix* y, Fp4Out* yo,
-                      float** part, uint16_t** gs, uint16_t** g3, uint16_t** t3, float** t,
-                      float** g) {
+struct Fp4BwdBuffers {
+  qlora_fp4_matrix y;  // q(dY)
+  Fp4Out yo;
+  float *t, *g;        // T where it is recomputed, G; up to kFp4SplitMaxM tokens in parts
+  float* part;         // split partial sums of the tensor-core rank products
+  uint16_t *gs, *g3, *t3;
+};
+size_t fp4_bwd_layout(const LinearShape& s, int format, void* ws, Fp4BwdBuffers* b) {
   Carve c(ws);
-  *y = carve_fp4(c, s.M, s.N, format, yo);
+  b->y = carve_fp4(c, s.M, s.N, format, &b->yo);
+  const bool few = s.M <= kFp4SplitMaxM;
+  const size_t mr = static_cast<size_t>(s.M) * s.r;
+  b->t = c.take<float>(mr * (few ? fp4_prep_parts(s.K) : 1));
+  b->g = c.take<float>(mr * (few ? fp4_prep_parts(s.N) : 1));
+  if (few) return c.off + 256;
   size_t pf = partial_floats(s.M, s.N, 64);                    // G = dY B^T
   pf = std::max(pf, partial_floats(s.M, s.K, 64));             // T = X A (recompute)
   pf = std::max(pf, partial_floats(stacked_rows(s.K, s.N), s.M, 192));  // dA and dB
-  *part = c.take<float>(pf);
-  *gs = c.take<uint16_t>(static_cast<size_t>(s.M) * 128);
-  *g3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
-  *t3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
-  *t = c.take<float>(static_cast<size_t>(s.M) * s.r);
-  *g = c.take<float>(static_cast<size_t>(s.M) * s.r);
+  b->part = c.take<float>(pf);
+  b->gs = c.take<uint16_t>(static_cast<size_t>(s.M) * 128);
+  b->g3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
+  b->t3 = c.take<uint16_t>(static_cast<size_t>(s.M) * 192);
   return c.off + 256;
+}
+
+// Up to kFp4SplitMaxM tokens: dY's rows and G in one launch, dX, dA with dB.
+qlora_status fp4_backward_few(const uint16_t* dY, const uint16_t* X, const float* T_saved,
+                              const qlora_fp4_matrix& wt, const uint16_t* A, const uint16_t* B,
+                              const LinearShape& s, uint16_t* dX, float* dA, float* dB,
+                              const Fp4BwdBuffers& b, cudaStream_t st) {
+  const int g_parts = fp4_prep_parts(s.N), t_parts = T_saved ? 1 : fp4_prep_parts(s.K);
+  if (!T_saved) QL_TRY(launch_fp4_prep(X, s.M, s.K, wt.format, nullptr, A, false, s.r, b.t, st));
+  QL_TRY(launch_fp4_prep(dY, s.M, s.N, wt.format, dX ? &b.yo : nullptr, B, true, s.r, b.g, st));
+  if (dX) {
+    const Fp4Ext ext{A, nullptr, b.g, g_parts, nullptr, s.r, s.scale, false};
+    const qlora_status q = fp4_product(b.y, wt, &ext, dX, false, true, st);
+    if (q != QLORA_OK) return q;
+  }
+  QL_TRY(launch_fp4_small_grads(X, dY, s.M, s.K, s.N, b.g, g_parts, T_saved ? T_saved : b.t, t_parts, s.r,
+                                s.scale, dA, dB, st));
+  return QLORA_OK;
 }
 }  // namespace
 
@@ -1340,11 +1366,8 @@ size_t fp4_fwd_workspace(const LinearShape& s, int format) {
 }
 
 size_t fp4_bwd_workspace(const LinearShape& s, int format) {
-  qlora_fp4_matrix y;
-  Fp4Out o;
-  float *p, *t, *g;
-  uint16_t *gs, *g3, *t3;
-  return fp4_bwd_layout(s, format, nullptr, &y, &o, &p, &gs, &g3, &t3, &t, &g);
+  Fp4BwdBuffers b;
+  return fp4_bwd_layout(s, format, nullptr, &b);
 }
 
 qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uint16_t* A,
@@ -1357,7 +1380,7 @@ qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uin
   fp4_fwd_layout(s, w.format, ws, &x, &xo, &part, &ts, &tbuf);
   Fp4Ext ext{B, nullptr, nullptr, 0, T_save, s.r, s.scale, true};
   if (s.M <= kFp4SplitMaxM) {
-    QL_TRY(launch_fp4_prep(X, s.M, s.K, w.format, xo, A, s.r, tbuf, st));
+    QL_TRY(launch_fp4_prep(X, s.M, s.K, w.format, &xo, A, false, s.r, tbuf, st));
     ext.t = tbuf;
     ext.t_parts = fp4_prep_parts(s.K);
     return fp4_product(x, w, &ext, Y, false, true, st);
@@ -1373,30 +1396,30 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
                           const qlora_fp4_matrix& wt, const uint16_t* A, const uint16_t* B,
                           const LinearShape& s, uint16_t* dX, float* dA, float* dB, void* ws,
                           cudaStream_t st) {
-  qlora_fp4_matrix y;
-  Fp4Out yo;
-  float *part, *tbuf, *gbuf;
-  uint16_t *gs, *g3, *t3;
-  fp4_bwd_layout(s, wt.format, ws, &y, &yo, &part, &gs, &g3, &t3, &tbuf, &gbuf);
+  Fp4BwdBuffers b;
+  fp4_bwd_layout(s, wt.format, ws, &b);
+  if (s.M <= kFp4SplitMaxM) return fp4_backward_few(dY, X, T_saved, wt, A, B, s, dX, dA, dB, b, st);
+  const qlora_fp4_matrix& y = b.y;
+  float* part = b.part;
   const float* t = T_saved;
   if (!t) {
-    qlora_status q = lora_down_T(X, A, s, part, tbuf, nullptr, st);
+    qlora_status q = lora_down_T(X, A, s, part, b.t, nullptr, st);
     if (q != QLORA_OK) return q;
-    t = tbuf;
+    t = b.t;
   }
-  if (dX) QL_TRY(launch_fp4_quantize(dY, true, s.M, s.N, wt.format, yo, st));
+  if (dX) QL_TRY(launch_fp4_quantize(dY, true, s.M, s.N, wt.format, b.yo, st));
   CUtensorMap ta, tb, ga, gb, ga1, gb1;
   int splits = 0;
   QL_MAP(&ta, kBF16, dY, s.N, s.M, s.N * 2, 64, 128, kSW128);  // dY K-major (over n)
   QL_MAP(&tb, kBF16, B, s.N, s.r, s.N * 2, 64, 64, kSW128);    // B [r, N] K-major
   QL_TRY((run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, st, &splits)));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
-                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, gbuf, gs, g3, t,
-                    t3, dX ? y.gscale : nullptr, dX ? wt.gscale : nullptr, 3));
+                    splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, b.gs, b.g3, t,
+                    b.t3, dX ? y.gscale : nullptr, dX ? wt.gscale : nullptr, 3));
   QL_MAP(&ga, kBF16, X, s.K, s.M, s.K * 2, 64, 64, kSW128);    // X as MN-major (k inner)
-  QL_MAP(&gb, kBF16, g3, 192, s.M, 384, 64, 64, kSW128);       // G in three parts, MN-major
+  QL_MAP(&gb, kBF16, b.g3, 192, s.M, 384, 64, 64, kSW128);       // G in three parts, MN-major
   QL_MAP(&ga1, kBF16, dY, s.N, s.M, s.N * 2, 64, 64, kSW128);  // dY as MN-major (n inner)
-  QL_MAP(&gb1, kBF16, t3, 192, s.M, 384, 64, 64, kSW128);      // T in three parts, MN-major
+  QL_MAP(&gb1, kBF16, b.t3, 192, s.M, 384, 64, 64, kSW128);      // T in three parts, MN-major
   // dA and dB beside dX, as in gemm_backward
   SideStream* side = nullptr;
   if (dX) QL_TRY(side_stream(st, &side));
@@ -1408,7 +1431,7 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   }
   qlora_status q = QLORA_OK;
   if (dX) {
-    const Fp4Ext ext{A, gs, gbuf, 1, nullptr, s.r, s.scale, false};
+    const Fp4Ext ext{A, b.gs, nullptr, 0, nullptr, s.r, s.scale, false};
     q = fp4_product(y, wt, &ext, dX, false, false, st);
   }
   cudaError_t e = cudaSuccess;

@@ -158,11 +158,15 @@ cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int6
                                        const Fp4Out& w, const Fp4Out& wt, void* ws,
                                        cudaStream_t st);
 cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st);
-// Few tokens (linear forward): quantizes X [M, K] bf16 to `out` and writes the parts of T = X A
-// over K, fp32 [fp4_prep_parts(K)][M][r], in one launch.
+// Few tokens: quantizes X [M, K] bf16 to `out` (unless NULL) and writes the parts over K of
+// T = X A, A [K, r] or (a_t) [r, K], fp32 [fp4_prep_parts(K)][M][r], in one launch.
 int fp4_prep_parts(int64_t K);
-cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out& out,
-                            const uint16_t* A, int r, float* T, cudaStream_t st);
+cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out* out,
+                            const uint16_t* A, bool a_t, int r, float* T, cudaStream_t st);
+// Few tokens: dA [K, r] = scale X^T G, dB [r, N] = scale T^T dY, G and T as sums of parts.
+cudaError_t launch_fp4_small_grads(const uint16_t* X, const uint16_t* dY, int64_t M, int64_t K, int64_t N,
+                                   const float* G, int g_parts, const float* T, int t_parts, int r,
+                                   float scale, float* dA, float* dB, cudaStream_t st);
 // The rank-r term added to a product a b^T: scale sum_j p[j, n] t[m, j]; p is [r, N]
 // (mn_major) or [N, r]. Above kFp4SplitMaxM tokens it is taken from q, bf16 hi | lo pairs
 // [M, 128] of scale t in units of the two gscales; up to there from t itself, the sum of
