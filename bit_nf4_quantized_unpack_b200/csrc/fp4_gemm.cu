@@ -298,22 +298,34 @@ __global__ void __launch_bounds__(kSplitThreads)
     if (cs > 1) cluster_sync_all();
     else __syncwarp();  // a warp reads only what it wrote
     if (got) {
-      for (int q = t0 + (lane >> 3); q < t1; q += 4) {
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+      constexpr int kAt = 2;  // tokens of a lane whose remote loads are in flight together
+      for (int q0 = t0 + (lane >> 3); q0 < t1; q0 += 4 * kAt) {
+        float4 sum[kAt];
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
         for (int c = 0; c < cs; ++c) {
-          const float4 v = ld_cluster_f32x4(part + q * 128 + r4, cs > 1 ? c : rank);
-          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+          float4 v[kAt];
+#pragma unroll
+          for (int i = 0; i < kAt; ++i)
+            v[i] = ld_cluster_f32x4(part + min(q0 + 4 * i, t1 - 1) * 128 + r4, cs > 1 ? c : rank);
+#pragma unroll
+          for (int i = 0; i < kAt; ++i)
+            sum[i].x += v[i].x, sum[i].y += v[i].y, sum[i].z += v[i].z, sum[i].w += v[i].w;
         }
-        if (p4 >= args.P) continue;  // P is a multiple of 8
-        const float gq = args.gq ? __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
-        const float4 o = make_float4(sum.x * g4[0] * gq, sum.y * g4[1] * gq, sum.z * g4[2] * gq,
-                                     sum.w * g4[3] * gq);
-        if (args.out_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(args.out) + q * args.ld + p4) = o;
-        else
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + q * args.ld + p4) =
-              make_uint2(pack_bf16x2_rn(o.x, o.y), pack_bf16x2_rn(o.z, o.w));
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+          const int q = q0 + 4 * i;
+          if (q >= t1 || p4 >= args.P) continue;  // P is a multiple of 8
+          const float gq = args.gq ? __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
+          const float4 o = make_float4(sum[i].x * g4[0] * gq, sum[i].y * g4[1] * gq,
+                                       sum[i].z * g4[2] * gq, sum[i].w * g4[3] * gq);
+          if (args.out_f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(args.out) + q * args.ld + p4) = o;
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.out) + q * args.ld + p4) =
+                make_uint2(pack_bf16x2_rn(o.x, o.y), pack_bf16x2_rn(o.z, o.w));
+        }
       }
     }
   }
@@ -331,56 +343,65 @@ __global__ void __launch_bounds__(kSplitThreads)
 }
 
 // ------------------------------------------------------------------ pair kernel
-// A persistent CTA pair per two SMs; a tile is 256 weight rows x 256 tokens. Each CTA holds 128
-// weight rows of the operand, 128 tokens of the other, its rows' scales and all 256 tokens'
-// scales, and accumulates its 128 rows x 256 tokens in its own tensor memory.
+// A persistent CTA pair per two SMs; a tile is 256 weight rows x TQ tokens (256, or 128 where
+// that gives more pairs work). Each CTA holds 128 weight rows of the operand, half of the
+// tokens of the other, its rows' scales and all tokens' scales, and accumulates its 128 rows
+// x TQ tokens in its own tensor memory.
 //
-// Tensor memory: two 256-column accumulators used in turn and two sets of scale columns. They
-// do not fit side by side (2 * 256 + 2 * 48 > 512), so the accumulators share the columns
-// [160, 256): the epilogue reads those first and then lets the next tile's MMAs start, while
-// it goes on with the other 160 columns.
+// Tensor memory: two accumulators of TQ columns used in turn and two sets of scale columns.
+// For TQ = 256 they do not fit side by side (2 * 256 + 2 * 48 > 512), so the accumulators
+// share the columns [160, 256): the epilogue reads those first and then lets the next tile's
+// MMAs start, while it goes on with the other 160 columns.
 //
 // Warp 0: TMA, warp 1: MMA (in the leader) and tensor memory, warps 2-9: epilogue, two warps
 // for each quarter of the lanes.
 constexpr int kPairThreads = 320;
-constexpr int kPairStages = 5;
-constexpr int kPairTile = 256;                // weight rows and tokens of a tile
-constexpr uint32_t kPairQBytes = 128 * 128;
+constexpr int kPairP = 256;                   // weight rows of a tile
 constexpr uint32_t kPairSf = 4 * kSfTile;     // scales of 128 rows and one step (NVFP4)
-constexpr uint32_t kPairStage = kPBytes + kPairQBytes + 3 * kPairSf;
-constexpr uint32_t kPairEpi = 8 * 2 * 32 * 32 * 2;
-constexpr uint32_t kPairSmem = 1024 + kPairStages * kPairStage + kPairEpi + 256;
-static_assert(kPairSmem <= 227 * 1024, "shared memory per CTA");
-constexpr uint32_t kAcc1 = 160;               // first column of the second accumulator
-constexpr uint32_t kSfCol = 416;              // first scale column; sets of 48
 constexpr int kEpiWarps = 8;
+constexpr uint32_t kPairEpi = kEpiWarps * 2 * 32 * 32 * 2;
+template <int TQ>
+struct Pair {
+  static constexpr int kStages = TQ == 256 ? 5 : 6;
+  static constexpr uint32_t kQBytes = TQ / 2 * 128;
+  static constexpr int kSqTiles = TQ / 128;   // token scale tiles
+  static constexpr uint32_t kStage = kPBytes + kQBytes + (1 + kSqTiles) * kPairSf;
+  static constexpr uint32_t kSmem = 1024 + kStages * kStage + kPairEpi + 256;
+  static constexpr bool kShared = TQ == 256;               // accumulators share columns
+  static constexpr uint32_t kAcc1 = TQ == 256 ? 160 : 128;  // first column of the second
+  static constexpr uint32_t kSfCol = kAcc1 + TQ;           // first scale column
+  static constexpr uint32_t kSfSet = 16 + 16 * kSqTiles;
+  static_assert(kSmem <= 227 * 1024 && kSfCol + 2 * kSfSet <= 512, "shared and tensor memory");
+};
 
 struct PairTile {
   int64_t p0, q0;
 };
 // Tiles in groups of eight token tiles, so that the tiles in flight at one time form a block
 // that shares operands in L2.
+template <int TQ>
 __device__ __forceinline__ PairTile pair_tile(int t, int p_tiles, int q_tiles) {
   constexpr int kGroup = 8;
   const int per = kGroup * p_tiles;
   const int g = t / per, in = t - g * per;
   const int width = min(kGroup, q_tiles - g * kGroup);
-  return {static_cast<int64_t>(in / width) * kPairTile,
-          static_cast<int64_t>(g * kGroup + in % width) * kPairTile};
+  return {static_cast<int64_t>(in / width) * kPairP, static_cast<int64_t>(g * kGroup + in % width) * TQ};
 }
 
-template <Fp4 F, bool OUT_F32>
+template <Fp4 F, int TQ, bool OUT_F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_fp4_gemm_pair(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_sp, const __grid_constant__ CUtensorMap tm_sq,
                     const __grid_constant__ CUtensorMap tm_ext_p,
                     const __grid_constant__ CUtensorMap tm_ext_q,
                     const __grid_constant__ CUtensorMap tm_out, const Fp4Args args) {
-  constexpr int S = kPairStages;
+  using C = Pair<TQ>;
+  constexpr int S = C::kStages;
+  constexpr uint32_t kPairQBytes = C::kQBytes;
   constexpr int kTileStep = kStepCols / kFp4TileCols<F>;  // scale tiles per step: 2 or 4
   constexpr int kMmaTile = 4 / kTileStep;                 // MMAs per scale tile: 2 or 1
   constexpr uint32_t kSfBytes = kTileStep * kSfTile;      // of 128 rows and one step
-  constexpr uint32_t kStepTx = 2 * (kPBytes + kPairQBytes + 3 * kSfBytes);  // both CTAs
+  constexpr uint32_t kStepTx = 2 * (kPBytes + kPairQBytes + (1 + C::kSqTiles) * kSfBytes);  // both CTAs
   constexpr uint32_t kExtTx = 2 * (kPBytes + kPairQBytes);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -389,8 +410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint8_t* q_s = p_s + S * kPBytes;             // [S][kPairQBytes]
   uint8_t* epi_s = q_s + S * kPairQBytes;       // [8 warps][2][32][32] bf16
   uint8_t* sfp_s = epi_s + kPairEpi;            // [S][kPairSf]
-  uint8_t* sfq_s = sfp_s + S * kPairSf;         // [S][2 kPairSf]: two row tiles, kSfBytes each
-  uint64_t* full = reinterpret_cast<uint64_t*>(sfq_s + S * 2 * kPairSf);  // the leader's counts
+  uint8_t* sfq_s = sfp_s + S * kPairSf;         // [S][kSqTiles kPairSf]: row tiles of kSfBytes
+  uint64_t* full = reinterpret_cast<uint64_t*>(sfq_s + S * C::kSqTiles * kPairSf);  // the leader's counts
   uint64_t* empty = full + S;                   // [S] MMAs reading the slot done (both CTAs)
   uint64_t* acc_full = empty + S;               // accumulator complete (both CTAs)
   uint64_t* acc_part = acc_full + 1;            // shared columns read out (the leader's counts)
@@ -400,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int q_tiles = static_cast<int>((args.Q + kPairTile - 1) / kPairTile);
+  const int q_tiles = static_cast<int>((args.Q + TQ - 1) / TQ);
   const int tiles = args.p_tiles * q_tiles;
   const int clusters = gridDim.x / 2, first = blockIdx.x / 2;
   const int my_tiles = first < tiles ? (tiles - 1 - first) / clusters + 1 : 0;
@@ -432,8 +453,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int n = 0;  // steps issued
       bool ok = true;
       for (int i = 0; i < my_tiles && ok; ++i) {
-        const PairTile t = pair_tile(first + i * clusters, args.p_tiles, q_tiles);
-        const int p0 = static_cast<int>(t.p0) + 128 * rank, q0 = static_cast<int>(t.q0) + 128 * rank;
+        const PairTile t = pair_tile<TQ>(first + i * clusters, args.p_tiles, q_tiles);
+        const int p0 = static_cast<int>(t.p0) + 128 * rank, q0 = static_cast<int>(t.q0) + TQ / 2 * rank;
         for (int k = 0; k < total; ++k, ++n) {
           const int s = n % S;
           if (n >= S && !mbar_wait(&empty[s], ((n / S) - 1) & 1u, abort_flag)) {
@@ -459,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tma_load_2d_pair(qs, &tm_q, bar, step * 128, q0);
             const int x = step * kTileStep * 64;  // in 8-byte elements
             tma_load_2d_pair(sfp_s + s * kPairSf, &tm_sp, bar, x, p0 / 128);
-            tma_load_2d_pair(sfq_s + s * 2 * kPairSf, &tm_sq, bar, x, static_cast<int>(t.q0 / 128));
+            tma_load_2d_pair(sfq_s + s * C::kSqTiles * kPairSf, &tm_sq, bar, x, static_cast<int>(t.q0 / 128));
           }
         }
       }
@@ -470,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
     if (rank == 0 && elect_one()) {
-      const uint32_t idesc_ext = idesc_bf16_f32(kPairTile, kPairTile, args.ext_mn, false);
+      const uint32_t idesc_ext = idesc_bf16_f32(kPairP, TQ, args.ext_mn, false);
       const uint32_t ext_adv = args.ext_mn ? 128u : 2u;
       // descriptors of slot 0; the start-address field counts 16 bytes
       const uint64_t dp0 = smem_desc_sw128(smem_u32(p_s), 16, 1024);
@@ -482,18 +503,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int n = 0;
       bool ok = true;
       for (int i = 0; i < my_tiles && ok; ++i) {
-        const uint32_t d = tmem + (i & 1) * kAcc1;
-        // The epilogue has the shared columns of tile i - 1 in registers (and, having begun
-        // that tile, all of tile i - 2, which used this accumulator).
-        if (i >= 1) ok = mbar_wait(acc_part, (i - 1) & 1u, abort_flag);
+        const uint32_t d = tmem + (i & 1) * C::kAcc1;
+        // Shared columns: the epilogue has those of tile i - 1 in registers (and, having begun
+        // that tile, all of tile i - 2, which used this accumulator). Otherwise: it has all of
+        // tile i - 2.
+        constexpr int kBack = C::kShared ? 1 : 2;
+        if (i >= kBack) ok = mbar_wait(acc_part, (i - kBack) & 1u, abort_flag);
         tc_fence_after();
         for (int k = 0; k < total && ok; ++k) {
           const int s = n % S;
           // The scale columns of this step were last read by the MMAs two steps ago (two sets,
           // used in turn), and MMAs of different kinds are not ordered with each other: wait
-          // for the completion of step n - 2, or of n - 1 where the kind changes. (At the
-          // start of a tile everything before it is complete: its epilogue has begun.)
-          const int before = ext && k == ext ? n - 1 : k >= ext + 2 ? n - 2 : -1;
+          // for the completion of step n - 2, or of n - 1 where the kind changes.
+          const int before = ext && (k == 0 || k == ext) ? n - 1 : n - 2;
           ok = before >= 0 ? mbar_wait_both(&full[s], (n / S) & 1u, &empty[before % S],
                                             (before / S) & 1u, abort_flag)
                            : mbar_wait(&full[s], (n / S) & 1u, abort_flag);
@@ -507,21 +529,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           } else {
             const uint64_t dp = dp0 + static_cast<uint32_t>(s) * (kPBytes >> 4);
             const uint64_t sp = dsp0 + static_cast<uint32_t>(s) * (kPairSf >> 4);
-            const uint64_t sq = dsq0 + static_cast<uint32_t>(s) * (2 * kPairSf >> 4);
-            const uint32_t sfp = tmem + kSfCol + (n & 1) * 48, sfq = sfp + 16;
+            const uint64_t sq = dsq0 + static_cast<uint32_t>(s) * (C::kSqTiles * kPairSf >> 4);
+            const uint32_t sfp = tmem + C::kSfCol + (n & 1) * C::kSfSet, sfq = sfp + 16;
             // scale tile tl and the MMAs that use it
             auto tile = [&](int tl, int mmas) {
               tmem_cp_scales_pair(sfp + tl * 4, sp + tl * (kSfTile >> 4));
-              tmem_cp_scales_pair(sfq + tl * 8, sq + tl * (kSfTile >> 4));
-              tmem_cp_scales_pair(sfq + tl * 8 + 4, sq + ((kSfBytes + tl * kSfTile) >> 4));
+#pragma unroll
+              for (int h = 0; h < C::kSqTiles; ++h)
+                tmem_cp_scales_pair(sfq + (tl * C::kSqTiles + h) * 4, sq + ((h * kSfBytes + tl * kSfTile) >> 4));
 #pragma unroll
               for (int sub = 0; sub < kMmaTile; ++sub) {
                 const int kk = tl * kMmaTile + sub;
                 if (kk < mmas)
                   umma_fp4_pair<F == Fp4::kMx ? 2 : 4>(
                       d, dp + kk * 2u, dq + kk * 2u,
-                      idesc_fp4(kPairTile, kPairTile, F == Fp4::kMx, F == Fp4::kMx ? 2 * sub : 0),
-                      sfp + tl * 4, sfq + tl * 8, (k | kk) != 0);
+                      idesc_fp4(kPairP, TQ, F == Fp4::kMx, F == Fp4::kMx ? 2 * sub : 0),
+                      sfp + tl * 4, sfq + tl * C::kSqTiles * 4, (k | kk) != 0);
               }
             };
             if (k < total - 1 || tail_mmas == 4) {
@@ -549,12 +572,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (lane == 0) tma_prefetch_desc(&tm_out);
     int chunks = 0;  // stage buffers used
     for (int i = 0; i < my_tiles; ++i) {
-      const PairTile t = pair_tile(first + i * clusters, args.p_tiles, q_tiles);
+      const PairTile t = pair_tile<TQ>(first + i * clusters, args.p_tiles, q_tiles);
       const int64_t p0 = t.p0 + 128 * rank + quarter * 32;
-      // this warp's four 32-token chunks: the shared columns first. Accumulator 0 shares its
-      // chunks 5-7, accumulator 1 its chunks 0-2.
+      // this warp's 32-token chunks, those in shared columns first: accumulator 0 shares its
+      // chunks 5-7, accumulator 1 its chunks 0-2
+      constexpr int kChunks = TQ / 64;
       const int shared0 = (i & 1) ? 0 : 5, own0 = (i & 1) ? 3 : 0;
-      const int c0 = shared0 + 2 * half, c1 = half ? own0 + 2 : shared0 + 1;
+      const int c0 = C::kShared ? shared0 + 2 * half : 2 * half;
+      const int c1 = C::kShared ? (half ? own0 + 2 : shared0 + 1) : 2 * half + 1;
       const int c2 = own0 + (half ? 3 : 0), c3 = own0 + (half ? 4 : 1);
       const int cs[4] = {c0, c1, c2, c3};
       float gq[4], gp[4];
@@ -562,7 +587,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int j = 0; j < 4; ++j) {
         gq[j] = 1.f;
         gp[j] = 1.f;
-        if (args.gq) gq[j] = __ldg(args.gq + (args.gq_rows ? min(t.q0 + cs[j] * 32 + lane, args.Q - 1) : 0));
+        if (args.gq && j < kChunks) gq[j] = __ldg(args.gq + (args.gq_rows ? min(t.q0 + cs[j] * 32 + lane, args.Q - 1) : 0));
         // rows lane / 4 + 8 j of the quarter (bf16 output), row lane (fp32 output, j = 0)
         const int64_t row = p0 + (OUT_F32 ? lane : (lane >> 2) + 8 * j);
         if (args.gp) gp[j] = __ldg(args.gp + (args.gp_rows ? min(row, args.P - 1) : 0));
@@ -572,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t taddr = tmem + (i & 1) * kAcc1 + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t taddr = tmem + (i & 1) * C::kAcc1 + (static_cast<uint32_t>(quarter * 32) << 16);
       // tensor memory -> registers: 32 rows x 32 tokens
       auto fetch = [&](int c, uint32_t (&v)[32]) {
         if constexpr (OUT_F32) {
@@ -634,24 +659,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ++chunks;
       };
       uint32_t v0[32], v1[32];
+      const bool both = !C::kShared || half == 0;  // before the hand-over
       fetch(c0, v0);
-      if (half == 0) fetch(c1, v1);
+      if (both) fetch(c1, v1);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(part_bar);
       emit(0, v0);
-      if (half != 0) {
+      if (!both) {
         fetch(c1, v1);
         tmem_ld_wait();
       }
       emit(1, v1);
-      fetch(c2, v0);
-      tmem_ld_wait();
-      emit(2, v0);
-      fetch(c3, v1);
-      tmem_ld_wait();
-      emit(3, v1);
+      if constexpr (kChunks == 4) {
+        fetch(c2, v0);
+        tmem_ld_wait();
+        emit(2, v0);
+        fetch(c3, v1);
+        tmem_ld_wait();
+        emit(3, v1);
+      }
     }
     if (elect_one()) bulk_wait_group_all();  // tile stores done before the CTA exits
   }
@@ -732,47 +760,55 @@ qlora_status run_split(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, con
   return QLORA_OK;
 }
 
-template <Fp4 F>
+template <Fp4 F, int TQ>
 qlora_status run_pair(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
                       Fp4Args args, cudaStream_t st) {
   CUtensorMap tp, tq, sp, sq, xp, xq, to;
   QL_MAP(&tp, kU8, b.codes, b.cols / 2, b.rows, b.cols / 2, 128, kPRows, kSw128);
-  QL_MAP(&tq, kU8, a.codes, a.cols / 2, a.rows, a.cols / 2, 128, 128, kSw128);
+  QL_MAP(&tq, kU8, a.codes, a.cols / 2, a.rows, a.cols / 2, 128, TQ / 2, kSw128);
   // scale tiles as rows of 8-byte elements: 64 per tile
   constexpr uint32_t box = kStepCols / kFp4TileCols<F> * 64;
   constexpr CUtensorMapDataType kU64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
   const uint64_t srow = static_cast<uint64_t>(args.ktiles) * 512;
   QL_MAP(&sp, kU64, b.scales, srow / 8, (b.rows + 127) / 128, srow, box, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
-  QL_MAP(&sq, kU64, a.scales, srow / 8, (a.rows + 127) / 128, srow, box, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+  QL_MAP(&sq, kU64, a.scales, srow / 8, (a.rows + 127) / 128, srow, box, TQ / 128, CU_TENSOR_MAP_SWIZZLE_NONE);
   xp = tp;
   xq = tq;
   if (ext) {
     if (ext->mn_major) QL_MAP(&xp, kBf16Map, ext->p, b.rows, ext->r, b.rows * 2, 64, 64, kSw128);
     else QL_MAP(&xp, kBf16Map, ext->p, ext->r, b.rows, ext->r * 2, 64, kPRows, kSw128);
-    QL_MAP(&xq, kBf16Map, ext->q, 128, a.rows, 256, 64, 128, kSw128);
+    QL_MAP(&xq, kBf16Map, ext->q, 128, a.rows, 256, 64, TQ / 2, kSw128);
   }
   if (args.out_f32)
     QL_MAP(&to, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, args.out, b.rows, a.rows, b.rows * 4, 32, 32,
            CU_TENSOR_MAP_SWIZZLE_NONE);
   else
     QL_MAP(&to, kBf16Map, args.out, b.rows, a.rows, b.rows * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-  args.p_tiles = static_cast<int>((b.rows + kPairTile - 1) / kPairTile);
-  const int64_t tiles = static_cast<int64_t>(args.p_tiles) * ((a.rows + kPairTile - 1) / kPairTile);
+  args.p_tiles = static_cast<int>((b.rows + kPairP - 1) / kPairP);
+  const int64_t tiles = static_cast<int64_t>(args.p_tiles) * ((a.rows + TQ - 1) / TQ);
   if (tiles > (int64_t{1} << 30)) {
     set_last_error("the product has too many tiles");
     return QLORA_ERR_SHAPE;
   }
-  auto kern = args.out_f32 ? k_fp4_gemm_pair<F, true> : k_fp4_gemm_pair<F, false>;
-  QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem));
+  auto kern = args.out_f32 ? k_fp4_gemm_pair<F, TQ, true> : k_fp4_gemm_pair<F, TQ, false>;
+  QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair<TQ>::kSmem));
   const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, num_sms() / 2));
-  QL_TRY(launch_pdl(kern, dim3(grid), dim3(kPairThreads), kPairSmem, st, tp, tq, sp, sq, xp, xq, to, args));
+  QL_TRY(launch_pdl(kern, dim3(grid), dim3(kPairThreads), Pair<TQ>::kSmem, st, tp, tq, sp, sq, xp, xq, to, args));
   return QLORA_OK;
 }
 
 template <Fp4 F>
 qlora_status run_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
                          const Fp4Args& args, bool early, cudaStream_t st) {
-  if (a.rows > kFp4SplitMaxM) return run_pair<F>(a, b, ext, args, st);
+  if (a.rows > kFp4SplitMaxM) {
+    // Narrow tiles where they take no more rounds of the CTA pairs than wide ones, that is,
+    // where wide ones leave half of the pairs idle. NVFP4, N = K = 4096: 512 tokens (32 wide or
+    // 64 narrow tiles on 74 pairs) 9.9 against 10.7 us wide; 1024 tokens 14.5 against 11.6.
+    const int64_t pt = (b.rows + kPairP - 1) / kPairP, pairs = std::max(num_sms() / 2, 1);
+    const int64_t wide = (pt * ((a.rows + 255) / 256) + pairs - 1) / pairs;
+    const int64_t narrow = (pt * ((a.rows + 127) / 128) + pairs - 1) / pairs;
+    return narrow <= wide ? run_pair<F, 128>(a, b, ext, args, st) : run_pair<F, 256>(a, b, ext, args, st);
+  }
   if (a.rows <= 32) return run_split<F, 32>(a, b, ext, args, early, st);
   if (a.rows <= 64) return run_split<F, 64>(a, b, ext, args, early, st);
   return run_split<F, 128>(a, b, ext, args, early, st);
