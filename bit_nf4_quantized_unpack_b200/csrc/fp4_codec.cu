@@ -447,77 +447,95 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
 static_assert(kPrepTok * kPrepCols == kPrepThreads && 8 * 256 * 4 <= kPrepTok * kPrepXPitch, "sums");
 
 // Few tokens: dA [K, r] = scale X^T G and dB [r, N] = scale T^T dY, G and T fp32 in parts
-// [parts][M][r]. A CTA takes 64 columns of X (or of dY) and all of the rank; a thread 4 x 4
-// outputs, tokens in order, in fp32. For up to 128 tokens this is a few microseconds of FMAs
-// and reads X and dY once; the tensor-core path needs two launches and splits G and T in parts.
-constexpr int kGradCols = 64, kGradTok = 32;
+// [parts][M][r]. A CTA takes 64 columns of X (or of dY) and all of the rank, in passes of 32
+// tokens whose successors are fetched meanwhile; a warp 16 x 32 outputs with mma.sync, G (T)
+// as three bf16 parts, which hold an fp32 value to its last bit. At 128 tokens an FMA version
+// was bound by shared memory (12 us for r = 64, K = N = 4096).
+constexpr int kGradCols = 64, kGradTok = 32, kGradPitch = 64 * 2 + 16;
 __global__ void __launch_bounds__(256)
     k_fp4_small_grads(const uint16_t* __restrict__ X, const uint16_t* __restrict__ dY, int M, int64_t K,
                       int64_t N, const float* __restrict__ G, int g_parts, const float* __restrict__ T,
                       int t_parts, int r, float scale, float* __restrict__ dA, float* __restrict__ dB) {
   griddep_wait_and_release();
-  __shared__ __align__(16) float xs[kGradTok][kGradCols], vs[kGradTok][64];
-  const int tid = threadIdx.x;
+  __shared__ __align__(16) uint8_t xs[kGradTok * kGradPitch], vs[3][kGradTok * kGradPitch];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t k_ctas = (K + kGradCols - 1) / kGradCols;
   const bool second = blockIdx.x >= k_ctas;
   const int64_t C = second ? N : K, c0 = (blockIdx.x - (second ? k_ctas : 0)) * kGradCols;
   const uint16_t* src = second ? dY : X;
   const float* val = second ? T : G;
   const int parts = second ? t_parts : g_parts;
-  const int a4 = (tid & 15) * 4, j4 = (tid >> 4) * 4;
+  const int lt = tid >> 3, lc = (tid & 7) * 8;  // what this thread stages: token, eight columns
+  uint4 w;
+  float v[8];
+  auto fetch = [&](int m0) {
+    const bool in = m0 + lt < M;
+    w = make_uint4(0u, 0u, 0u, 0u);
+    if (in && c0 + lc < C) w = __ldg(reinterpret_cast<const uint4*>(src + (m0 + lt) * C + c0 + lc));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    if (in && lc < r) {
+      const float* p = val + static_cast<int64_t>(m0 + lt) * r + lc;
+#pragma unroll 2
+      for (int i = 0; i < parts; ++i, p += static_cast<int64_t>(M) * r) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+    }
+  };
+  const int wc = (warp & 3) * 16, wj = (warp >> 2) * 32;  // this warp's outputs
+  const uint32_t xa = smem_u32(xs) + (((lane >> 4) * 8 + (lane & 7)) * kGradPitch + (wc + ((lane >> 3) & 1) * 8) * 2);
+  const uint32_t va = smem_u32(vs[0]) + ((lane & 15) * kGradPitch + (wj + (lane >> 4) * 8) * 2);
   float acc[4][4] = {};
+  fetch(0);
   for (int m0 = 0; m0 < M; m0 += kGradTok) {
-    const int len = min(kGradTok, M - m0);
     __syncthreads();
-    {
-      const int t = tid >> 3, c = (tid & 7) * 8;  // 32 tokens x 8 groups of 8 columns
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (t < len && c0 + c < C) w = __ldg(reinterpret_cast<const uint4*>(src + (m0 + t) * C + c0 + c));
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    *reinterpret_cast<uint4*>(xs + lt * kGradPitch + lc * 2) = w;
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+      uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xs[t][c + 2 * i] = __uint_as_float(ww[i] << 16);
-        xs[t][c + 2 * i + 1] = __uint_as_float(ww[i] & 0xFFFF0000u);
+        q[i] = pack_bf16x2_rn(v[2 * i], v[2 * i + 1]);
+        v[2 * i] -= __uint_as_float(q[i] << 16);
+        v[2 * i + 1] -= __uint_as_float(q[i] & 0xFFFF0000u);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = c + 4 * h;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < len && j < r)
-          for (int p = 0; p < parts; ++p) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(
-                val + (static_cast<int64_t>(p) * M + m0 + t) * r + j));
-            v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
-          }
-        *reinterpret_cast<float4*>(&vs[t][j]) = v;
-      }
+      *reinterpret_cast<uint4*>(vs[part] + lt * kGradPitch + lc * 2) = make_uint4(q[0], q[1], q[2], q[3]);
     }
     __syncthreads();
-    if (j4 < r) {
-#pragma unroll 8
-      for (int t = 0; t < len; ++t) {
-        const float4 x = *reinterpret_cast<const float4*>(&xs[t][a4]);
-        const float4 v = *reinterpret_cast<const float4*>(&vs[t][j4]);
-        const float xa[4] = {x.x, x.y, x.z, x.w}, va[4] = {v.x, v.y, v.z, v.w};
+    if (m0 + kGradTok < M) fetch(m0 + kGradTok);
+    if (wj < r) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int t = 0; t < kGradTok; t += 16) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(xa + t * kGradPitch, a);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xa[i], va[j], acc[i][j]);
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(va + part * (kGradTok * kGradPitch) + t * kGradPitch + h * 32, b);
+            mma_16816(acc[2 * h], a, b[0], b[1]);
+            mma_16816(acc[2 * h + 1], a, b[2], b[3]);
+          }
       }
     }
   }
-  if (j4 >= r || c0 + a4 >= C) return;  // C is a multiple of 32, r of 8
-  if (!second) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(dA + (c0 + a4 + i) * r + j4) =
-          make_float4(scale * acc[i][0], scale * acc[i][1], scale * acc[i][2], scale * acc[i][3]);
-  } else {
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(dB + (j4 + j) * N + c0 + a4) =
-          make_float4(scale * acc[0][j], scale * acc[1][j], scale * acc[2][j], scale * acc[3][j]);
-  }
+    for (int e = 0; e < 4; e += 2) {
+      const int64_t c = c0 + wc + (lane >> 2) + 4 * e;  // rows lane / 4 and, for e = 2, eight on
+      const int j = wj + i * 8 + (lane & 3) * 2;
+      if (c >= C || j >= r) continue;
+      if (!second) {
+        *reinterpret_cast<float2*>(dA + c * r + j) = make_float2(scale * acc[i][e], scale * acc[i][e + 1]);
+      } else {
+        dB[j * N + c] = scale * acc[i][e];
+        dB[(j + 1) * N + c] = scale * acc[i][e + 1];
+      }
+    }
 }
 
 // ------------------------------------------------------------------ weights, square blocks
@@ -769,11 +787,8 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
               : u == 2 ? k_fp4_quantize_nv<BF16, 2>
               : u == 4 ? k_fp4_quantize_nv<BF16, BF16 ? 4 : 0>
                        : k_fp4_quantize_nv<BF16, 0>;
-  // as many CTAs as run at one time
-  int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * std::max(per_sm, 1));
+  // about as many CTAs as run at one time
+  const int64_t grid = std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * (1536 / threads));
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, st, X,
                     static_cast<uint32_t>(rows), cols, codes, scales, gscale);
 }

@@ -233,13 +233,13 @@ __global__ void __launch_bounds__(kSplitThreads)
     const int Q = static_cast<int>(args.Q);
     if (ext) {
       // scale t / (ga gb) as bf16 hi and lo parts in the K-major swizzled operand layout
-      const float gb = args.gp ? *args.gp : 1.f;
+      const float ib = args.gp ? 1.f / *args.gp : 1.f;
 #pragma unroll 4
       for (int i = tid; i < NT * 8; i += 128) {  // eight values of a token: one 16-byte group
         const int q = i >> 3, j = (i & 7) * 8;
         float v[8] = {};
         if (q < Q && j < sa.r) {
-          const float ga = args.gq ? __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
+          const float ia = args.gq ? 1.f / __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
 #pragma unroll 4
           for (int part = 0; part < sa.t_parts; ++part) {
             const float4* src =
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kSplitThreads)
             dst[1] = make_float4(v[4], v[5], v[6], v[7]);
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = v[k] * sa.scale / ga / gb;
+          for (int k = 0; k < 8; ++k) v[k] = v[k] * sa.scale * ia * ib;
         }
         uint32_t hi[4], lo[4];
 #pragma unroll

@@ -766,7 +766,14 @@ __global__ void k_finalize_rank(const float* __restrict__ part, int splits, int6
   const int64_t stride = rows_pad * 64;
   int sp = 0;
   float v1 = 0.f, v2 = 0.f, v3 = 0.f;
-  for (; sp + 4 <= splits; sp += 4) {  // four independent loads in flight
+  for (; sp + 16 <= splits; sp += 16) {  // 16 loads in flight, added in the order of the loop below
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = p[(sp + i) * stride];
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) v += x[i], v1 += x[i + 1], v2 += x[i + 2], v3 += x[i + 3];
+  }
+  for (; sp + 4 <= splits; sp += 4) {
     v += p[sp * stride];
     v1 += p[(sp + 1) * stride];
     v2 += p[(sp + 2) * stride];
@@ -809,6 +816,7 @@ __global__ void __launch_bounds__(256)
   const int64_t stride = rows_pad * 64;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   const float* p = part + srow0 * 64 + threadIdx.x;  // item u: srow0 * 64 + threadIdx.x + 256 u
+#pragma unroll 4
   for (int sp = 0; sp < splits; ++sp) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) v[u] += p[sp * stride + 256 * u];
