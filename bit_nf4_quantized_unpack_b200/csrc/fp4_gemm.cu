@@ -792,7 +792,10 @@ qlora_status run_pair(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, cons
   }
   auto kern = args.out_f32 ? k_fp4_gemm_pair<F, TQ, true> : k_fp4_gemm_pair<F, TQ, false>;
   QL_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pair<TQ>::kSmem));
-  const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, num_sms() / 2));
+  // the fewest pairs that take no more rounds than all of them: the others' SMs are left to a
+  // kernel beside this one (dA and dB), their share of L2 bandwidth and power to these
+  const int64_t pairs = std::max(num_sms() / 2, 1), rounds = (tiles + pairs - 1) / pairs;
+  const int grid = 2 * static_cast<int>((tiles + rounds - 1) / rounds);
   QL_TRY(launch_pdl(kern, dim3(grid), dim3(kPairThreads), Pair<TQ>::kSmem, st, tp, tq, sp, sq, xp, xq, to, args));
   return QLORA_OK;
 }
