@@ -181,3 +181,28 @@ def test_empty():
     for fmt in FMTS:
         q = qlora.qlora_fp4_quantize(x, fmt)
         assert qlora.qlora_fp4_dequant(q).shape == (0, 64)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(fmt):
+    """A matrix of more than 2^32 bytes: its last rows, whose offsets need 64 bits."""
+    rows, cols = 70001, 32768                      # 2.3e9 bf16 values
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pick = [0, 32767, 32768, 65535, 65536, 69999, 70000]
+    x.zero_()
+    for i in pick:
+        x[i] = torch.randn(cols, generator=g, device="cuda").to(torch.bfloat16) * 2.0 ** (i % 5)
+    q = qlora.qlora_fp4_quantize(x, fmt)
+    v = qlora.qlora_fp4_dequant(q)
+    ref = F.quantize(x[pick].double().cpu().numpy(), fmt)
+    want = torch.from_numpy(F.dequant(ref)).to(torch.bfloat16)
+    assert torch.equal(v[pick].cpu(), want)
+    for i, row in enumerate(pick):
+        assert np.array_equal(q.codes[row].cpu().numpy(), F.pack(ref["codes"][i:i + 1])[0])
+    # and as the operand of a product: the last rows' tokens
+    w = qlora.qlora_fp4_quantize(torch.eye(32, cols, device="cuda"), fmt)
+    one = F.dequant(F.quantize(np.eye(1, 32), fmt))[0, 0]  # what the format stores for 1
+    out = qlora.qlora_fp4_matmul(q, w, torch.float32)
+    assert torch.equal(out[pick].cpu(), want[:, :32].float() * float(one))  # exact products
+    assert not out[1:32767].any()

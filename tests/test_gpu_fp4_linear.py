@@ -66,6 +66,27 @@ def test_matmul(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [
+    (2600, 4128, 288),     # several rounds of the CTA pairs, accumulators in turn, K ends in a step
+    (300, 12544, 160),     # several rounds of narrow tiles
+    (130, 256, 32),        # one tile, one MMA
+    (8, 20000, 2304),      # more weight tiles than SMs, two CTAs to an SM
+    (128, 24576, 320),     # the same with one CTA to an SM
+    (40, 128, 8192),       # one tile, its K shared by eight CTAs
+])
+def test_matmul_schedules(M, N, K, fmt):
+    a, b = normal(M + K, M, K).cuda(), normal(N, N, K, std=0.02).cuda()
+    qa, qb = qlora.qlora_fp4_quantize(a, fmt), qlora.qlora_fp4_quantize(b, fmt)
+    va, vb = (qlora.qlora_fp4_dequant(q, torch.float32).double() for q in (qa, qb))
+    want = (va @ vb.t()).cpu().numpy()
+    tol = (K / 64 + 8) * U * (va.abs() @ vb.abs().t()).cpu().numpy()
+    for _ in range(2):
+        got = qlora.qlora_fp4_matmul(qa, qb, torch.float32)
+        within(got, want, tol, "fp32")
+    within(qlora.qlora_fp4_matmul(qa, qb), want, tol + BF16 * (np.abs(want) + tol), "bf16")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_matmul_reads_every_scale_in_its_place(fmt):
     """One-hot codes under scales that all differ: each output is one product of a code and two
     scales, exact in fp32."""
@@ -157,8 +178,21 @@ def test_linear(M, N, K, r, fmt):
     check_layer(M, N, K, r, fmt)
 
 
-def test_linear_recomputes_T():
-    check_layer(70, 160, 320, 16, qlora.FP4_NVFP4, saved_T=False)
+@pytest.mark.parametrize("M", [1, 70, 200])
+def test_linear_recomputes_T(M):
+    check_layer(M, 160, 320, 16, qlora.FP4_NVFP4, saved_T=False)
+
+
+@pytest.mark.parametrize("M,N,K,r", [
+    (2, 96, 8256, 8),         # T in three parts of K
+    (100, 8256, 96, 64),      # G in three parts of N
+    (2600, 4128, 288, 24),    # several rounds with the rank-r steps, forward
+    (2600, 288, 4128, 64),    # and for dX
+    (300, 12544, 160, 40),
+    (17, 20000, 64, 16),
+])
+def test_linear_schedules(M, N, K, r):
+    check_layer(M, N, K, r, qlora.FP4_NVFP4 if r != 24 else qlora.FP4_MXFP4)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -193,6 +227,64 @@ def test_empty_batch_and_partial_outputs():
     assert none is None and torch.equal(dA, full[1]) and torch.equal(dB, full[2])
     Y1, none = qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0, save_T=False)
     assert none is None and torch.equal(Y1, qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0)[0])
+
+
+def test_layer_after_its_weight_in_one_stream():
+    """The forward fetches its weight ahead of its tokens, but never before the kernels that
+    wrote it: laying a new weight out into the same storage and using it at once, repeatedly."""
+    M, N, K, r = 4, 2048, 1024, 8
+    W, A, B, X, dY = (t.cuda() for t in layer(31, M, N, K, r, 1))
+    ws = [W, W.flip(0).contiguous(), W * 2]
+    want = []
+    for w in ws:
+        q = qlora.qlora_fp4_quantize_weight(w)
+        torch.cuda.synchronize()
+        y, t = qlora.qlora_fp4_linear_fwd(X, q, A, B, 0.5)
+        want.append((y, qlora.qlora_fp4_linear_bwd(dY, X, t, q, A, B, 0.5)[0]))
+        torch.cuda.synchronize()
+    q = qlora.qlora_fp4_quantize_weight(W)
+    for i in range(12):
+        qlora.qlora_fp4_quantize_weight(ws[i % 3], out=q)
+        y, t = qlora.qlora_fp4_linear_fwd(X, q, A, B, 0.5)
+        dx = qlora.qlora_fp4_linear_bwd(dY, X, t, q, A, B, 0.5)[0]
+        assert torch.equal(y, want[i % 3][0]) and torch.equal(dx, want[i % 3][1])
+
+
+def test_caller_buffers_and_refusals_on_the_device():
+    M, N, K, r = 20, 64, 96, 8
+    W, A, B, X, dY = (t.cuda() for t in layer(41, M, N, K, r, 1))
+    q = qlora.qlora_fp4_quantize_weight(W)
+    Y, T = qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0)
+    ws = torch.empty(qlora.qlora_fp4_linear_fwd_workspace_size(M, N, K, r), dtype=torch.uint8, device="cuda")
+    Y1, T1 = torch.empty_like(Y), torch.empty_like(T)
+    got = qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0, Y=Y1, T=T1, workspace=ws)
+    assert got[0] is Y1 or got[0].data_ptr() == Y1.data_ptr()
+    assert torch.equal(Y1, Y) and torch.equal(T1, T)
+    with pytest.raises(qlora.QLoraError):
+        qlora.qlora_fp4_linear_fwd(X, q, A, B, 1.0, workspace=ws[:16])
+    with pytest.raises(qlora.QLoraError):                      # r = 12
+        qlora.qlora_fp4_linear_fwd(X, q, torch.zeros(K, 12, dtype=torch.bfloat16, device="cuda"),
+                                   torch.zeros(12, N, dtype=torch.bfloat16, device="cuda"), 1.0)
+    with pytest.raises(qlora.QLoraError):                      # a misaligned address
+        qlora.qlora_fp4_quantize(torch.zeros(33, device="cuda")[1:].view(1, 32))
+    with pytest.raises(ValueError):
+        qlora.qlora_fp4_linear_fwd(X[:, :64].contiguous(), q, A, B, 1.0)
+    with pytest.raises(ValueError):
+        qlora.qlora_fp4_linear_fwd(X, q, A.cpu(), B, 1.0)
+    with pytest.raises(ValueError):
+        qlora.qlora_fp4_quantize(W.t())
+    with pytest.raises(TypeError):
+        qlora.qlora_fp4_quantize(W.half())
+    with pytest.raises(TypeError):
+        qlora.qlora_fp4_dequant(q.w, torch.float16)
+    short = qlora.FP4Matrix(q.w.codes, q.w.scales[:512], q.w.gscale, 256, K, 1)
+    with pytest.raises(ValueError):
+        qlora.qlora_fp4_dequant(short)
+    with pytest.raises(ValueError):
+        qlora.qlora_fp4_linear_bwd(dY, X, T, qlora.FP4Weight(q.w), A, B, 1.0)
+    mx = qlora.qlora_fp4_quantize(X, qlora.FP4_MXFP4)
+    with pytest.raises(qlora.QLoraError):
+        qlora.qlora_fp4_matmul(mx, q.w)
 
 
 def test_streams_and_graphs():
