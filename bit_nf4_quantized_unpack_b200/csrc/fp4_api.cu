@@ -6,6 +6,9 @@ namespace qlora {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 256;  // tile coordinates are 32-bit
+// A CTA pair multiplies 256 columns in about 0.4 us, and no role of a kernel may wait for
+// another one longer than the 2 s after which waits give up: 2^28 columns take 0.4 s.
+constexpr int64_t kMaxCols = int64_t{1} << 28;
 constexpr int64_t kMaxValues = int64_t{1} << 40;        // grid dimensions of the codec kernels
 constexpr int64_t kMaxWeightRows = int64_t{65535} * 32;  // the weight kernel's grid
 constexpr size_t kWeightWorkspace = 256;
@@ -14,7 +17,7 @@ bool known_format(int32_t f) { return f == QLORA_FP4_MX || f == QLORA_FP4_NV; }
 bool known_dtype(qlora_dtype d) { return d == QLORA_F32 || d == QLORA_BF16; }
 
 qlora_status check_shape(int64_t rows, int64_t cols) {
-  if (rows < 0 || rows > kMaxRows || cols < 32 || cols > kMaxRows || cols % 32 != 0)
+  if (rows < 0 || rows > kMaxRows || cols < 32 || cols > kMaxCols || cols % 32 != 0)
     return QLORA_ERR_SHAPE;
   if (rows > kMaxValues / cols) return QLORA_ERR_SHAPE;
   return QLORA_OK;

@@ -413,9 +413,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint8_t* sfq_s = sfp_s + S * kPairSf;         // [S][kSqTiles kPairSf]: row tiles of kSfBytes
   uint64_t* full = reinterpret_cast<uint64_t*>(sfq_s + S * C::kSqTiles * kPairSf);  // the leader's counts
   uint64_t* empty = full + S;                   // [S] MMAs reading the slot done (both CTAs)
-  uint64_t* acc_full = empty + S;               // accumulator complete (both CTAs)
-  uint64_t* acc_part = acc_full + 1;            // shared columns read out (the leader's counts)
-  uint64_t* mma_drain = acc_part + 1;
+  // of the tile in accumulator 0 or 1 (two of each, so that no waiter is ever two phases behind)
+  uint64_t* acc_full = empty + S;               // [2] complete (both CTAs)
+  uint64_t* acc_part = acc_full + 2;            // [2] handed over by the epilogue (the leader's)
+  uint64_t* mma_drain = acc_part + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -433,8 +434,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_part, 2 * kEpiWarps);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&acc_full[h], 1);
+      mbar_init(&acc_part[h], 2 * kEpiWarps);
+    }
     mbar_init(mma_drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -508,7 +511,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // that tile, all of tile i - 2, which used this accumulator). Otherwise: it has all of
         // tile i - 2.
         constexpr int kBack = C::kShared ? 1 : 2;
-        if (i >= kBack) ok = mbar_wait(acc_part, (i - kBack) & 1u, abort_flag);
+        if (i >= kBack)
+          ok = mbar_wait(&acc_part[(i - kBack) & 1], ((i - kBack) >> 1) & 1u, abort_flag);
         tc_fence_after();
         for (int k = 0; k < total && ok; ++k) {
           const int s = n % S;
@@ -557,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
           }
           umma_commit_pair(&empty[s]);
-          if (k == total - 1) umma_commit_pair(acc_full);
+          if (k == total - 1) umma_commit_pair(&acc_full[i & 1]);
           ++n;
         }
       }
@@ -568,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stage2 = epi_s + (warp - 2) * (2 * 32 * 32 * 2);
-    const uint32_t part_bar = cluster_addr(acc_part, 0);
+    const uint32_t part_bar = cluster_addr(acc_part, 0);  // of accumulator 0
     if (lane == 0) tma_prefetch_desc(&tm_out);
     int chunks = 0;  // stage buffers used
     for (int i = 0; i < my_tiles; ++i) {
@@ -592,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int64_t row = p0 + (OUT_F32 ? lane : (lane >> 2) + 8 * j);
         if (args.gp) gp[j] = __ldg(args.gp + (args.gp_rows ? min(row, args.P - 1) : 0));
       }
-      if (!mbar_wait(acc_full, i & 1u, abort_flag)) {
+      if (!mbar_wait(&acc_full[i & 1], (i >> 1) & 1u, abort_flag)) {
         if (!*abort_flag) record_error(args.err, abort_flag, kErrTimeoutEpilogue);
         break;
       }
@@ -665,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(part_bar);
+      if (lane == 0) mbar_arrive_cluster(part_bar + (i & 1) * 8);
       emit(0, v0);
       if (!both) {
         fetch(c1, v1);

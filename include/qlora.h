@@ -435,7 +435,7 @@ size_t qlora_fp4_scales_bytes(int64_t rows, int64_t cols, int32_t format);
  * enter rowmax.
  *   codes, scales as above; gscale fp32 [rows] (NV; not used and may be NULL for MX)
  * rows == 0 enqueues nothing. Errors: QLORA_ERR_SHAPE unless 0 <= rows < 2^31 - 256,
- * 32 <= cols < 2^31, cols % 32 == 0 and rows * cols <= 2^40; QLORA_ERR_INVALID_ARG for a NULL
+ * 32 <= cols <= 2^28, cols % 32 == 0 and rows * cols <= 2^40; QLORA_ERR_INVALID_ARG for a NULL
  * pointer, an unknown dtype or format; QLORA_ERR_ALIGN unless the pointers are 16-byte aligned.
  */
 qlora_status qlora_fp4_quantize(const void *X, qlora_dtype x_dtype, int64_t rows, int64_t cols,
@@ -489,7 +489,8 @@ size_t qlora_fp4_linear_fwd_workspace_size(int64_t M, int64_t n_out, int64_t k_i
  * q() is qlora_fp4_quantize in the weight's format; the LoRA term sees the 16-bit X. w is
  * [N, K] of qlora_fp4_quantize_weight (or any with one gscale), N % 32 == 0. Other arguments,
  * layouts and errors as qlora_linear_fwd. The LoRA term is carried in units of the gscales:
- * |scale T B| / (gscale of the row * gscale of w) has to stay in fp32's range.
+ * a given gscale of w has to be a normal non-zero number, and
+ * |scale T| / (gscale of the row * gscale of w) has to stay in bf16's range.
  */
 qlora_status qlora_fp4_linear_fwd(const uint16_t *X, int64_t M, qlora_fp4_matrix w,
                                   const uint16_t *A, const uint16_t *B, int r, float scale,

@@ -26,6 +26,7 @@ def test_scales_bytes(L):
     assert f(128, 64, 1) == 512 and f(129, 64, 1) == 1024 and f(128, 96, 1) == 1024
     assert f(128, 128, 0) == 512 and f(1, 160, 0) == 1024 and f(0, 64, 0) == 0
     assert f(1, 48, 1) == 0 and f(1, 0, 1) == 0 and f(-1, 32, 1) == 0 and f(1, 32, 2) == 0
+    assert f(1, 1 << 28, 0) == (1 << 28) // 128 * 512 and f(1, (1 << 28) + 32, 0) == 0
     assert f(1 << 31, 32, 1) == 0 and f(1 << 20, (1 << 20) + 32, 1) == 0
 
 

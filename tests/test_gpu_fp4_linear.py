@@ -69,6 +69,8 @@ def test_matmul(M, N, K, fmt):
 @pytest.mark.parametrize("M,N,K", [
     (2600, 4128, 288),     # several rounds of the CTA pairs, accumulators in turn, K ends in a step
     (300, 12544, 160),     # several rounds of narrow tiles
+    (300, 50176, 32),      # many rounds of one step, narrow and (below) wide
+    (8000, 2048, 32),
     (130, 256, 32),        # one tile, one MMA
     (8, 20000, 2304),      # more weight tiles than SMs, two CTAs to an SM
     (128, 24576, 320),     # the same with one CTA to an SM
