@@ -787,10 +787,11 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
               : u == 2 ? k_fp4_quantize_nv<BF16, 2>
               : u == 4 ? k_fp4_quantize_nv<BF16, BF16 ? 4 : 0>
                        : k_fp4_quantize_nv<BF16, 0>;
-  // with one chunk a thread about as many CTAs as run at one time, which fetch their next rows
-  // ahead (4096 x 4096: 11.9 us; a CTA a row 13.2); else a CTA a row (8192 x 11008: 48.6 us;
-  // resident CTAs 50.1, with their next rows in registers 59.5)
-  const int64_t grid = u == 1 ? std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * (1536 / threads)) : rows;
+  // One chunk a thread: about as many CTAs as run at one time, which fetch their next rows ahead
+  // (bf16 4096 x 4096 11.9 us; a CTA a row 13.2). More: a CTA a row for bf16 (8192 x 11008
+  // 48.6 us; resident CTAs 50.1), resident CTAs for fp32 (80.5 against 85.7 us).
+  const bool resident = u == 1 || !BF16;
+  const int64_t grid = resident ? std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * (1536 / threads)) : rows;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, st, X,
                     static_cast<uint32_t>(rows), cols, codes, scales, gscale);
 }
