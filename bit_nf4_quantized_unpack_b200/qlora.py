@@ -533,6 +533,12 @@ class FP4Weight:
     wt: FP4Matrix | None = None
 
 
+def _check_mx_out(q: FP4Matrix) -> None:
+    """Nothing writes the gscale of an MXFP4 output, but a product would multiply by it."""
+    if q.fmt == FP4_MXFP4 and q.gscale is not None:
+        raise ValueError("out.gscale: an MXFP4 matrix is quantized without one")
+
+
 def qlora_fp4_quantize(X: torch.Tensor, fmt: int = FP4_NVFP4,
                        out: FP4Matrix | None = None) -> FP4Matrix:
     """X [rows, cols] (fp32 or bf16, CUDA, contiguous) to microscaled form, each row by
@@ -544,6 +550,7 @@ def qlora_fp4_quantize(X: torch.Tensor, fmt: int = FP4_NVFP4,
         return FP4Matrix(c, s, g, rows, cols, fmt)
     if (out.rows, out.cols, out.fmt) != (*X.shape, fmt):
         raise ValueError("out: another shape or format than X")
+    _check_mx_out(out)
     ext.quantize_out(X, fmt, out.codes, out.scales, out.gscale)
     return out
 
@@ -564,6 +571,7 @@ def qlora_fp4_quantize_weight(W: torch.Tensor, fmt: int = FP4_NVFP4, transposed:
     if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
             wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):
         raise ValueError("out: another shape or format than W")
+    _check_mx_out(w)
     ext.weight_out(W, fmt, w.codes, w.scales, w.gscale, wt.codes if wt else None,
                    wt.scales if wt else None, workspace)
     if wt is not None:

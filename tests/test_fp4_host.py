@@ -117,3 +117,15 @@ def test_binding_refuses_what_it_cannot_pass_on():
         qlora.qlora_fp4_matmul(q, q)
     with pytest.raises(ValueError):
         qlora.qlora_fp4_linear_bwd(x, x, None, qlora.FP4Weight(q), x, x, 1.0)
+
+
+def test_mxfp4_output_with_a_gscale_is_refused():
+    """Quantizing to MXFP4 writes no gscale, and a product would multiply by the one left there."""
+    q = qlora.FP4Matrix.empty(64, 64, qlora.FP4_MXFP4, device="cpu")
+    q.gscale = torch.full((64,), 3.0)
+    with pytest.raises(ValueError, match="gscale"):
+        qlora.qlora_fp4_quantize(torch.zeros(64, 64), qlora.FP4_MXFP4, out=q)
+    q.gscale = q.gscale[:1]
+    with pytest.raises(ValueError, match="gscale"):
+        qlora.qlora_fp4_quantize_weight(torch.zeros(64, 64), qlora.FP4_MXFP4, transposed=False,
+                                        out=qlora.FP4Weight(q))
