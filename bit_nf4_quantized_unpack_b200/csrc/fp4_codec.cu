@@ -26,6 +26,11 @@ constexpr int kChunk = 16;  // values per thread and step: 32 bytes of bf16, 64 
 constexpr uint32_t kMag = 0x7FFFFFFFu;
 constexpr uint32_t kInf = 0x7F800000u;
 
+// Both bf16 halves of w times 2^64, for values small enough that this is exact.
+__device__ __forceinline__ void bf16x2_up64(uint32_t& w) {
+  w = pack_bf16x2_rn(__uint_as_float(w << 16) * 0x1p64f, __uint_as_float(w & 0xFFFF0000u) * 0x1p64f);
+}
+
 // 16 values as loaded, and their largest magnitude as fp32 bits (kInf or above when one of
 // them is not finite: magnitudes order like unsigned integers, NaNs last).
 template <bool BF16>
@@ -41,6 +46,10 @@ struct Raw16<true> {
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void scale_2_64() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bf16x2_up64(w[i]);
   }
   __device__ __forceinline__ float at(int i) const {
     return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
@@ -66,6 +75,10 @@ struct Raw16<false> {
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  }
+  __device__ __forceinline__ void scale_2_64() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= 0x1p64f;
   }
   __device__ __forceinline__ float at(int i) const { return v[i]; }
   __device__ __forceinline__ uint32_t amax() const {
@@ -95,6 +108,13 @@ __device__ __forceinline__ float div_rn(float x, float d, float rcp) {
   return __fmaf_rn(__fmaf_rn(-q, d, x), rcp, q);
 }
 
+// 1 / x to one ulp, for x that is neither subnormal nor larger than 2^126.
+__device__ __forceinline__ float rcp_1ulp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Scale byte of a block from its largest magnitude; g_inv = 1 / gscale (NVFP4).
 template <Fp4 F>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t am, float g_inv) {
@@ -106,18 +126,35 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t am, float g_inv) {
   return e4m3_bits(div_rn(__uint_as_float(am) * g_inv, 6.f, 1.f / 6.f));
 }
 
-// What turns a value into the argument of e2m1() under one scale byte.
+// An NVFP4 gscale 2^e and what encoders divide by: their own is 2^64 times as large for a
+// tiny one (1 / (g c) would overflow below 2^-118), and so are the values then.
+struct Gscale {
+  float g, inv, up;
+  __device__ __forceinline__ explicit Gscale(int e)
+      : g(pow2_f32(e)), inv(pow2_f32(-e)), up(e < -90 ? 0x1p64f : 1.f) {}
+  __device__ __forceinline__ float enc() const { return g * up; }
+  __device__ __forceinline__ float enc_inv() const { return up == 1.f ? inv : inv * 0x1p-64f; }
+};
+
+// What turns a value into the argument of e2m1() under one scale byte c. MX: x * mul. NV: the
+// quotient x / (g c) as q = x mul, mul = 1 / (g c) nearly, corrected by its remainder,
+// y = q + (x - q g c) mul. c has 4 significant bits, so the remainder is exact although mul is
+// off by an ulp or two, and y is the rounding of a number within 2^-20 ulp of the real
+// quotient. It is a border of e2m1() (3 bits) just where the quotient is one: elsewhere x and
+// the border times g c are different multiples of an ulp of x, which puts the quotient at
+// least 8/15 ulp off. What is computed is -q and -y, for the sign of a zero x, and the codes'
+// signs are turned at the end.
 template <Fp4 F>
 struct Encoder {
-  float mul, div, rcp;  // MX: x * mul; NV: x * mul / div, mul = 0 for codes that are all 0
-  __device__ __forceinline__ Encoder(uint32_t sb, float g_inv) {
+  float mul, div;  // NV: -1 / (g c), g c; mul = 0 for codes that are all 0
+  __device__ __forceinline__ Encoder(uint32_t sb, const Gscale& g) {
     if (F == Fp4::kMx) {
       mul = sb == kFp4NanScale<F> ? 0.f : pow2_f32(127 - static_cast<int>(sb));
     } else {
       const bool none = sb == 0u || sb == kFp4NanScale<F>;
-      mul = none ? 0.f : g_inv;
-      div = none ? 1.f : fp4_scale_value<F>(sb);
-      rcp = __frcp_rn(div);
+      const float c = none ? 1.f : fp4_scale_value<F>(sb);
+      mul = none ? 0.f : -rcp_1ulp(c) * g.enc_inv();
+      div = c * g.enc();
     }
   }
   __device__ __forceinline__ bool zero() const { return mul == 0.f; }
@@ -128,23 +165,23 @@ struct Encoder {
     if (F == Fp4::kMx) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = v(i) * mul;
-    } else {
-      const uint64_t m2 = f2_pack(mul, mul), r2 = f2_pack(rcp, rcp), d2 = f2_pack(-div, -div);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {  // div_rn on pairs
-        const uint64_t x = f2_mul(f2_pack(v(i), v(i + 1)), m2);
-        const uint64_t q = f2_mul(x, r2);
-        f2_unpack(f2_fma(f2_fma(q, d2, x), r2, q), y[i], y[i + 1]);
-      }
+      return fp4_pack8(y);
     }
-    return fp4_pack8(y);
+    const uint64_t m2 = f2_pack(mul, mul), d2 = f2_pack(div, div);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t x = f2_pack(v(i), v(i + 1)), q = f2_mul(x, m2);
+      f2_unpack(f2_fma(f2_fma(q, d2, x), m2, q), y[i], y[i + 1]);
+    }
+    return fp4_pack8(y) ^ 0x88888888u;
   }
 };
 
 // Codes of 16 values under one scale byte (low nibble first).
 template <Fp4 F, typename R>
-__device__ __forceinline__ uint2 codes16(const R& r, uint32_t sb, float g_inv) {
-  const Encoder<F> e(sb, g_inv);
+__device__ __forceinline__ uint2 codes16(R& r, uint32_t sb, const Gscale& g) {
+  if (F == Fp4::kNv && g.up != 1.f) r.scale_2_64();  // the same in every thread of a row
+  const Encoder<F> e(sb, g);
   if (e.zero()) return make_uint2(0u, 0u);
   return make_uint2(e.encode8([&](int i) { return r.at(i); }),
                     e.encode8([&](int i) { return r.at(8 + i); }));
@@ -181,7 +218,7 @@ __global__ void __launch_bounds__(256)
     am = max(am, __shfl_xor_sync(~0u, am, 1));
     const uint32_t sb = in ? scale_byte<Fp4::kMx>(am, 1.f) : 0u;
     if (in)
-      *reinterpret_cast<uint2*>(codes + (row * cols + col) / 2) = codes16<Fp4::kMx>(r, sb, 1.f);
+      *reinterpret_cast<uint2*>(codes + (row * cols + col) / 2) = codes16<Fp4::kMx>(r, sb, Gscale(0));
     const uint32_t w = gather4<Fp4::kMx>(sb);
     if ((lane & 7) == 0 && in)
       *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, col / 32, (cols + 127) / 128)) = w;
@@ -238,16 +275,15 @@ __global__ void __launch_bounds__(512)
     top = __reduce_max_sync(~0u, top);
     if ((tid & 31) == 0) part[pass][tid >> 5] = top;
     __syncthreads();  // a warp writes part[pass] again only past the next pass's barrier
-    for (int w = 0; w < (nt >> 5); ++w) top = max(top, part[pass][w]);
-    const int e = nv_gscale_exp(top);
-    if (tid == 0) gscale[row] = pow2_f32(e);
-    const float g_inv = pow2_f32(-e);
-    auto emit = [&](int c, const Raw16<BF16>& r, uint32_t m) {
+    top = __reduce_max_sync(~0u, (tid & 31) < (nt >> 5) ? part[pass][tid & 31] : 0u);  // 16 warps at most
+    const Gscale g(nv_gscale_exp(top));
+    if (tid == 0) gscale[row] = g.g;
+    auto emit = [&](int c, Raw16<BF16>& r, uint32_t m) {
       const bool in = c < chunks;
-      const uint32_t sb = in ? scale_byte<Fp4::kNv>(m, g_inv) : 0u;
+      const uint32_t sb = in ? scale_byte<Fp4::kNv>(m, g.inv) : 0u;
       if (in)
         *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<int64_t>(c) * (kChunk / 2)) =
-            codes16<Fp4::kNv>(r, sb, g_inv);
+            codes16<Fp4::kNv>(r, sb, g);
       const uint32_t w = gather4<Fp4::kNv>(sb);
       if ((c & 3) == 0 && c < padded)
         *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, c, ktiles)) = w;
@@ -286,7 +322,7 @@ __device__ __forceinline__ void quantize_row(const uint16_t* __restrict__ X, int
     }
   };
   fetch(0);
-  float g_inv = 1.f;
+  Gscale g(0);
   if constexpr (F == Fp4::kNv) {
     uint32_t top = 0u;
     for (int base = 0;;) {
@@ -303,11 +339,9 @@ __device__ __forceinline__ void quantize_row(const uint16_t* __restrict__ X, int
     top = __reduce_max_sync(~0u, top);
     if ((tid & 31) == 0) part[tid >> 5] = top;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) top = max(top, part[w]);
-    const int e = nv_gscale_exp(top);
-    if (tid == 0) gscale[row] = pow2_f32(e);
-    g_inv = pow2_f32(-e);
+    top = __reduce_max_sync(~0u, part[tid & (NT / 32 - 1)]);
+    g = Gscale(nv_gscale_exp(top));
+    if (tid == 0) gscale[row] = g.g;
     if (chunks > U * NT) fetch(0);
   }
   for (int base = 0; base < padded; base += U * NT) {
@@ -318,10 +352,10 @@ __device__ __forceinline__ void quantize_row(const uint16_t* __restrict__ X, int
       if (base + u * NT >= padded) break;  // the same in every thread
       uint32_t am = raw[u].amax();
       if (F == Fp4::kMx) am = max(am, __shfl_xor_sync(~0u, am, 1));
-      const uint32_t sb = c < chunks ? scale_byte<F>(am, g_inv) : 0u;
+      const uint32_t sb = c < chunks ? scale_byte<F>(am, g.inv) : 0u;
       if (c < chunks)
         *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<int64_t>(c) * (kChunk / 2)) =
-            codes16<F>(raw[u], sb, g_inv);
+            codes16<F>(raw[u], sb, g);
       const uint32_t w = gather4<F>(sb);
       if (c % kGroup == 0 && c < padded)
         *reinterpret_cast<uint32_t*>(scales + fp4_scale_offset(row, c * kChunk / kFp4Block<F>, padded / kGroup)) = w;
@@ -605,11 +639,10 @@ __global__ void __launch_bounds__(32 * kWeightWarps)
   const int64_t k0 = (static_cast<int64_t>(blockIdx.x) * kWeightWarps + (threadIdx.x >> 5)) * 64;
   const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 32;
   if (k0 >= k) return;
-  float g_inv = 1.f;
+  Gscale g(0);
   if (F == Fp4::kNv) {
-    const int e = nv_gscale_exp(__ldg(top));
-    g_inv = pow2_f32(-e);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *gscale = pow2_f32(e);
+    g = Gscale(nv_gscale_exp(__ldg(top)));
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *gscale = g.g;
   }
   const int64_t gk = k0 + kl * 8, gn = n0 + nl * 8;
   const bool in = gk < k;  // n is a multiple of 32, k of 32
@@ -659,8 +692,20 @@ __global__ void __launch_bounds__(32 * kWeightWarps)
     am = max(am, __shfl_xor_sync(~0u, am, 2));
     am = max(am, __shfl_xor_sync(~0u, am, 16));
   }
-  const uint32_t sb = in ? scale_byte<F>(am, g_inv) : 0u;
-  const Encoder<F> enc(sb, g_inv);
+  const uint32_t sb = in ? scale_byte<F>(am, g.inv) : 0u;
+  if (F == Fp4::kNv && g.up != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (BF16) {
+        bf16x2_up64(rb[i].x), bf16x2_up64(rb[i].y), bf16x2_up64(rb[i].z), bf16x2_up64(rb[i].w);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          rf[2 * i + h].x *= 0x1p64f, rf[2 * i + h].y *= 0x1p64f, rf[2 * i + h].z *= 0x1p64f, rf[2 * i + h].w *= 0x1p64f;
+      }
+    }
+  }
+  const Encoder<F> enc(sb, g);
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -778,19 +823,22 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
     return launch_pdl(k_fp4_quantize_mx<BF16>, grid, dim3(256), 0, st, X,
                       static_cast<uint32_t>(rows), cols, codes, scales);
   }
-  // chunks a thread: as few as 512 threads (256 where one is enough) allow, while the row
-  // fits the registers (32 a chunk of bf16 with its temporaries, 64 of fp32)
+  // Chunks a thread, while the row fits the registers: two, as more and smaller CTAs cover each
+  // other's barriers (bf16 4096 x 4096: 9.1 us, 12.8 with one chunk and 256 threads, 10.3 with
+  // four), four where two take more than 512 threads. Up to 1024 columns one, for at least a
+  // warp or two (8192 x 1024: 7.3 us; two chunks 9.2).
   const int64_t padded = (cols / kChunk + 3) & ~int64_t{3};
-  const int u = padded <= 256 ? 1 : padded <= 1024 ? 2 : padded <= 2048 && BF16 ? 4 : 0;
+  const int u = padded <= 64 ? 1 : padded <= 1024 ? 2 : padded <= 2048 && BF16 ? 4 : 0;
   const int threads = u == 0 ? 512 : static_cast<int>(((padded + u - 1) / u + 31) / 32 * 32);
   auto kern = u == 1   ? k_fp4_quantize_nv<BF16, 1>
               : u == 2 ? k_fp4_quantize_nv<BF16, 2>
               : u == 4 ? k_fp4_quantize_nv<BF16, BF16 ? 4 : 0>
                        : k_fp4_quantize_nv<BF16, 0>;
-  // One chunk a thread: about as many CTAs as run at one time, which fetch their next rows ahead
-  // (bf16 4096 x 4096 11.9 us; a CTA a row 13.2). More: a CTA a row for bf16 (8192 x 11008
-  // 48.6 us; resident CTAs 50.1), resident CTAs for fp32 (80.5 against 85.7 us).
-  const bool resident = u == 1 || !BF16;
+  // A CTA a row; as many CTAs as run at one time, each taking several rows, where a row is short
+  // (they fetch the next one ahead; 4096 x 1024: 4.4 us against 4.8) and where the registers of
+  // fp32 leave room for few CTAs (8192 x 11008: 73 us against 79; at 256 threads a CTA a row is
+  // better: 4096 x 8192 24.8 us against 28.0).
+  const bool resident = u == 1 || (u > 0 && !BF16 && threads > 256);
   const int64_t grid = resident ? std::min<int64_t>(rows, static_cast<int64_t>(num_sms()) * (1536 / threads)) : rows;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, st, X,
                     static_cast<uint32_t>(rows), cols, codes, scales, gscale);

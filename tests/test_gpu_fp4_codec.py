@@ -206,3 +206,37 @@ def test_offsets_past_32_bits(fmt):
     out = qlora.qlora_fp4_matmul(q, w, torch.float32)
     assert torch.equal(out[pick].cpu(), want[:, :32].float() * float(one))  # exact products
     assert not out[1:32767].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_signs_of_zeros(fmt, dtype):
+    """A negative zero, and a negative value that rounds to zero, keep the sign bit."""
+    x = draw(64, 128, 12, spread=1)
+    x[:, ::3] = -0.0
+    x[:, 1::3] *= 2.0 ** -12
+    x[:, 2::6] = 0.0
+    x = x.to(dtype)
+    q = check_rows(x, fmt)
+    assert (q.codes.cpu() & 15 == 8).any()
+    w = qlora.qlora_fp4_quantize_weight(x.cuda(), fmt)
+    ref, ref_t = F.quantize_weight(x.double().numpy(), fmt)
+    same_matrix(w.w, ref)
+    same_matrix(w.wt, ref_t)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tiny_and_huge_rows(fmt):
+    """gscales over their whole range, 2^-126 to 2^116, with blocks far below each row's top, and
+    fp32 values beside the borders."""
+    g = np.random.default_rng(31)
+    e = np.arange(-126, 118, 2)
+    x = torch.from_numpy(g.normal(0, 1, (e.size, 128))).float()
+    x[:, 64:] *= 2.0 ** -6
+    x[:, 0] = 2000.0
+    x = (x.double() * torch.from_numpy(2.0 ** e.astype(np.float64))[:, None]).float()
+    check_rows(x, fmt)
+    for row in (0, 10, 17, 18, 19, 60, e.size - 1):
+        W = x[row].repeat(32, 1)[:, :32].contiguous()
+        w = qlora.qlora_fp4_quantize_weight(W.cuda(), fmt)
+        same_matrix(w.w, F.quantize_weight(W.double().numpy(), fmt)[0], row)
