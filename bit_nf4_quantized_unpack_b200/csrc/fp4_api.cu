@@ -11,7 +11,7 @@ constexpr int64_t kMaxRows = (int64_t{1} << 31) - 256;  // tile coordinates are 
 constexpr int64_t kMaxCols = int64_t{1} << 28;
 constexpr int64_t kMaxValues = int64_t{1} << 40;        // grid dimensions of the codec kernels
 constexpr int64_t kMaxWeightRows = int64_t{65535} * 32;  // the weight kernel's grid
-constexpr size_t kWeightWorkspace = 256;
+constexpr size_t kWeightWorkspace = kFp4MaxTops * sizeof(uint32_t);
 
 bool known_format(int32_t f) { return f == QLORA_FP4_MX || f == QLORA_FP4_NV; }
 bool known_dtype(qlora_dtype d) { return d == QLORA_F32 || d == QLORA_BF16; }

@@ -573,25 +573,28 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ weights, square blocks
-constexpr int kAmaxChunks = 4;  // per thread, all in flight
-// Largest finite magnitude of the matrix, as fp32 bits in *top (zero before the launch). One
-// atomic per CTA: one per warp on the single address took longer than the reading.
+// Largest finite magnitudes, as fp32 bits, of what each CTA reads: *parts[gridDim.x]. One CTA
+// per SM, so that who needs the matrix's maximum has few to join, and nothing has to be zero
+// before the launch.
+constexpr int kAmaxThreads = 1024;
 template <bool BF16>
-__global__ void __launch_bounds__(256)
-    k_fp4_amax(const void* __restrict__ W, int64_t chunks, uint32_t* __restrict__ top) {
+constexpr int kAmaxChunks = BF16 ? 4 : 2;  // per thread, all in flight: 128 bytes
+template <bool BF16>
+__global__ void __launch_bounds__(kAmaxThreads)
+    k_fp4_amax(const void* __restrict__ W, int64_t chunks, uint32_t* __restrict__ parts) {
   griddep_wait_and_release();
-  __shared__ uint32_t part[8];
+  __shared__ uint32_t part[32];
   uint32_t m = 0u;
-  constexpr int64_t kBatch = 256 * kAmaxChunks;
+  constexpr int64_t kBatch = kAmaxThreads * kAmaxChunks<BF16>;
   for (int64_t c0 = blockIdx.x * kBatch + threadIdx.x; c0 < chunks; c0 += gridDim.x * kBatch) {
-    Raw16<BF16> r[kAmaxChunks];
+    Raw16<BF16> r[kAmaxChunks<BF16>];
 #pragma unroll
-    for (int u = 0; u < kAmaxChunks; ++u) {
-      if (c0 + u * 256 < chunks) r[u].load(W, (c0 + u * 256) * kChunk);
+    for (int u = 0; u < kAmaxChunks<BF16>; ++u) {
+      if (c0 + u * kAmaxThreads < chunks) r[u].load(W, (c0 + u * kAmaxThreads) * kChunk);
       else r[u].zero();
     }
 #pragma unroll
-    for (int u = 0; u < kAmaxChunks; ++u) {
+    for (int u = 0; u < kAmaxChunks<BF16>; ++u) {
       const uint32_t a = r[u].amax();
       m = max(m, a < kInf ? a : finite_amax(r[u]));
     }
@@ -599,10 +602,9 @@ __global__ void __launch_bounds__(256)
   m = __reduce_max_sync(~0u, m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) m = max(m, part[w]);
-    if (m) atomicMax(top, m);  // a maximum: no order to depend on
+  if (threadIdx.x < 32) {
+    m = __reduce_max_sync(~0u, part[threadIdx.x]);
+    if (threadIdx.x == 0) parts[blockIdx.x] = m;
   }
 }
 
@@ -622,27 +624,30 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
   }
 }
 
-constexpr int kWeightWarps = 4;  // of a CTA; eight were 7 % slower
-// A warp takes 32 rows x 64 columns of W, a lane 8 x 8 of it (lane = row group * 8 + column
+// A CTA is one warp (four were 3-10 % slower in bf16, the same in fp32) and takes 32 rows x
+// 64 columns of W, a lane 8 x 8 of it (lane = row group * 8 + column
 // group), so that squares of 16 and of 32 are whole in the warp: the maxima go through
 // shuffles, the transposed codes through an 8 x 8 nibble transpose in registers. The
 // transposed copy has the same squares, so it stores the same values.
 template <Fp4 F, bool BF16>
-__global__ void __launch_bounds__(32 * kWeightWarps)
+__global__ void __launch_bounds__(32)
     k_fp4_quantize_weight(const void* __restrict__ W, int64_t n, int64_t k,
-                          const uint32_t* __restrict__ top, uint8_t* __restrict__ codes,
+                          const uint32_t* tops, int ntops, uint8_t* __restrict__ codes,
                           uint8_t* __restrict__ scales, float* __restrict__ gscale,
                           uint8_t* __restrict__ t_codes, uint8_t* __restrict__ t_scales) {
   griddep_wait_and_release();
   constexpr int B = kFp4Block<F>;
-  const int lane = threadIdx.x & 31, kl = lane & 7, nl = lane >> 3;
-  const int64_t k0 = (static_cast<int64_t>(blockIdx.x) * kWeightWarps + (threadIdx.x >> 5)) * 64;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.y) * 32;
-  if (k0 >= k) return;
+  const int lane = threadIdx.x, kl = lane & 7, nl = lane >> 3;
+  const int64_t k0 = static_cast<int64_t>(blockIdx.x) * 64;
+  // NVFP4: from the last rows, which k_fp4_amax left in L2 (fp32 11008 x 4096: 70.9 us, from
+  // the first 75.8)
+  const int64_t n0 = static_cast<int64_t>(F == Fp4::kNv ? gridDim.y - 1 - blockIdx.y : blockIdx.y) * 32;
   Gscale g(0);
   if (F == Fp4::kNv) {
-    g = Gscale(nv_gscale_exp(__ldg(top)));
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *gscale = g.g;
+    uint32_t top = 0u;
+    for (int i = lane; i < ntops; i += 32) top = max(top, __ldg(tops + i));
+    g = Gscale(nv_gscale_exp(__reduce_max_sync(~0u, top)));
+    if (blockIdx.x == 0 && blockIdx.y == 0 && lane == 0) *gscale = g.g;
   }
   const int64_t gk = k0 + kl * 8, gn = n0 + nl * 8;
   const bool in = gk < k;  // n is a multiple of 32, k of 32
@@ -846,22 +851,18 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
 
 template <bool BF16>
 cudaError_t quantize_weight(const void* W, int64_t n, int64_t k, int format, const Fp4Out& w,
-                            const Fp4Out& wt, uint32_t* top, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((k + 64 * kWeightWarps - 1) / (64 * kWeightWarps)), static_cast<unsigned>(n / 32));
+                            const Fp4Out& wt, uint32_t* tops, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((k + 63) / 64), static_cast<unsigned>(n / 32));
   if (format == QLORA_FP4_MX)
-    return launch_pdl(k_fp4_quantize_weight<Fp4::kMx, BF16>, grid, dim3(32 * kWeightWarps), 0, st, W, n, k,
-                      static_cast<const uint32_t*>(nullptr), w.codes, w.scales, w.gscale, wt.codes,
+    return launch_pdl(k_fp4_quantize_weight<Fp4::kMx, BF16>, grid, dim3(32), 0, st, W, n, k,
+                      static_cast<const uint32_t*>(nullptr), 0, w.codes, w.scales, w.gscale, wt.codes,
                       wt.scales);
-  cudaError_t e = cudaMemsetAsync(top, 0, sizeof(uint32_t), st);
+  const int64_t chunks = n * k / kChunk, batch = kAmaxThreads * kAmaxChunks<BF16>;
+  const int ctas = static_cast<int>(std::min<int64_t>({(chunks + batch - 1) / batch, num_sms(), kFp4MaxTops}));
+  const cudaError_t e = launch_pdl(k_fp4_amax<BF16>, dim3(ctas), dim3(kAmaxThreads), 0, st, W, chunks, tops);
   if (e != cudaSuccess) return e;
-  const int64_t chunks = n * k / kChunk;
-  const int64_t blocks = std::min<int64_t>((chunks + 256 * kAmaxChunks - 1) / (256 * kAmaxChunks),
-                                           static_cast<int64_t>(num_sms()) * 8);
-  e = launch_pdl(k_fp4_amax<BF16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, W, chunks,
-                 top);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_fp4_quantize_weight<Fp4::kNv, BF16>, grid, dim3(32 * kWeightWarps), 0, st, W, n, k,
-                    static_cast<const uint32_t*>(top), w.codes, w.scales, w.gscale, wt.codes,
+  return launch_pdl(k_fp4_quantize_weight<Fp4::kNv, BF16>, grid, dim3(32), 0, st, W, n, k,
+                    static_cast<const uint32_t*>(tops), ctas, w.codes, w.scales, w.gscale, wt.codes,
                     wt.scales);
 }
 
@@ -881,9 +882,9 @@ cudaError_t launch_fp4_quantize(const void* X, bool bf16, int64_t rows, int64_t 
 cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int64_t k, int format,
                                        const Fp4Out& w, const Fp4Out& wt, void* ws,
                                        cudaStream_t st) {
-  uint32_t* top = static_cast<uint32_t*>(ws);
-  return bf16 ? quantize_weight<true>(W, n, k, format, w, wt, top, st)
-              : quantize_weight<false>(W, n, k, format, w, wt, top, st);
+  uint32_t* tops = static_cast<uint32_t*>(ws);
+  return bf16 ? quantize_weight<true>(W, n, k, format, w, wt, tops, st)
+              : quantize_weight<false>(W, n, k, format, w, wt, tops, st);
 }
 
 int fp4_prep_parts(int64_t K) { return static_cast<int>((K + 8 * kPrepSlice - 1) / (8 * kPrepSlice)); }

@@ -154,6 +154,8 @@ inline size_t fp4_scales_bytes(int64_t rows, int64_t cols, int format) {
 }
 cudaError_t launch_fp4_quantize(const void* X, bool bf16, int64_t rows, int64_t cols, int format,
                                 const Fp4Out& out, cudaStream_t st);
+// ws: room for kFp4MaxTops words.
+constexpr int kFp4MaxTops = 256;
 cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int64_t k, int format,
                                        const Fp4Out& w, const Fp4Out& wt, void* ws,
                                        cudaStream_t st);
