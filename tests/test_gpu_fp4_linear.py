@@ -322,6 +322,52 @@ def test_streams_and_graphs():
             assert all(torch.equal(x, y) for x, y in zip(out, ref))
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_large_batch_on_streams_and_in_graphs(fmt):
+    """A batch whose quantizer runs beside the rank-r product: against the formulas, on two
+    streams at once, in a replayed graph, and in a graph captured by a thread that has made no
+    call before (which has no side stream and runs everything in order)."""
+    import threading
+    check_layer(1100, 96, 160, 16, fmt)
+    W, A, B, X, dY = (t.cuda() for t in layer(13, 1100, 96, 160, 16, fmt))
+    q = qlora.qlora_fp4_quantize_weight(W, fmt)
+
+    def step(x, dy):
+        y, t = qlora.qlora_fp4_linear_fwd(x, q, A, B, 0.5)
+        return (y, t) + qlora.qlora_fp4_linear_bwd(dy, x, t, q, A, B, 0.5)
+    X2, dY2 = X.flip(0).contiguous(), dY.flip(0).contiguous()
+    want, want2 = step(X, dY), step(X2, dY2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = {}
+    for _ in range(3):
+        for name, s, args in (("a", s1, (X, dY)), ("b", s2, (X2, dY2))):
+            with torch.cuda.stream(s):
+                got[name] = step(*args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got["a"], want))
+    assert all(torch.equal(x, y) for x, y in zip(got["b"], want2))
+    bx, bdy = X.clone(), dY.clone()
+    made = []
+
+    def capture():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(bx, bdy)
+        made.append((graph, out))
+    capture()
+    t = threading.Thread(target=capture)
+    t.start()
+    t.join()
+    assert len(made) == 2
+    for graph, out in made:
+        for src, ref in (((X2, dY2), want2), ((X, dY), want)):
+            bx.copy_(src[0]), bdy.copy_(src[1])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(out, ref))
+
+
 def test_training_step_on_a_microscaled_weight():
     """The operators together: lay the weight out, forward, backward, optimizer step, and the
     next forward on the updated adapter."""
