@@ -781,6 +781,7 @@ __global__ void __launch_bounds__(256)
   const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
   const float g = gscale ? __ldg(gscale + (g_per_row ? row : 0)) : 1.f;
+  const uint64_t g2 = f2_pack(g, g);
   for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * 1024; c0 < cols; c0 += static_cast<int64_t>(gridDim.y) * 1024) {
     uint32_t w[U], sb[U];
 #pragma unroll
@@ -799,12 +800,14 @@ __global__ void __launch_bounds__(256)
       const int64_t col = c0 + (u * 32 + lane) * V;
       if (col >= cols) break;
       const float s = fp4_scale_value<F>(sb[u]);
+      const uint64_t s2 = f2_pack(s, s);
       float v[V];
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         const float2 f = e2m1_pair(w[u] >> (8 * j));
-        v[2 * j] = f.x * s * g;
-        v[2 * j + 1] = f.y * s * g;
+        uint64_t x = f2_mul(f2_pack(f.x, f.y), s2);
+        if (F == Fp4::kNv || gscale) x = f2_mul(x, g2);  // MXFP4 has none as a rule
+        f2_unpack(x, v[2 * j], v[2 * j + 1]);
       }
       if constexpr (BF16)
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * cols + col) =
