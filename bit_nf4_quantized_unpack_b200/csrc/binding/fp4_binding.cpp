@@ -105,6 +105,23 @@ Tensor make(at::IntArrayRef shape, at::ScalarType dtype, c10::DeviceIndex dev) {
   return at::empty(shape, at::TensorOptions().dtype(dtype).device(c10::Device(c10::kCUDA, dev)));
 }
 
+// `bytes` of one allocation, handed out as uint8 tensors at multiples of 256 bytes (an
+// allocation costs the host a microsecond). All of one type, as tensors of different types on one
+// storage cannot be saved together.
+struct Bytes {
+  Tensor all;
+  int64_t off = 0;
+  static int64_t room(int64_t n) { return (n + 255) / 256 * 256; }
+  Bytes(int64_t bytes, c10::DeviceIndex dev) : all(make({bytes}, at::kByte, dev)) {}
+  Tensor take(at::IntArrayRef shape) {
+    auto t = c10::make_intrusive<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+    t->set_storage_offset(off);
+    t->set_sizes_contiguous(shape);
+    off += room(t->numel());
+    return Tensor(std::move(t));
+  }
+};
+
 // The operands' device made current, and its current stream.
 struct Launch {
   c10::cuda::CUDAGuard guard;
@@ -164,8 +181,9 @@ py::tuple quantize(const Tensor& X, int fmt) {
   const void* x = dense(X, "X", dev, X.scalar_type(), X.sizes());
   const size_t nsc = L.scales_bytes(rows, cols, fmt);
   if (nsc == 0 && rows != 0) check(QLORA_ERR_SHAPE, "qlora_fp4_quantize");
-  Tensor codes = make({rows, cols / 2}, at::kByte, dev);
-  Tensor scales = make({static_cast<int64_t>(nsc)}, at::kByte, dev);
+  const int64_t sc = static_cast<int64_t>(nsc);
+  Bytes b(Bytes::room(rows * (cols / 2)) + sc, dev);
+  const Tensor codes = b.take({rows, cols / 2}), scales = b.take({sc});
   Tensor g;
   if (fmt == QLORA_FP4_NV) g = make({rows}, at::kFloat, dev);
   const Launch l(dev);
@@ -220,15 +238,19 @@ py::tuple weight(const Tensor& W, int fmt, bool transposed, const OptTensor& wor
   const int64_t n = W.size(0), k = W.size(1);
   const size_t nsc = L.scales_bytes(n, k, fmt), tsc = L.scales_bytes(k, n, fmt);
   if (nsc == 0 || (transposed && tsc == 0)) check(QLORA_ERR_SHAPE, "qlora_fp4_quantize_weight");
-  Tensor codes = make({n, k / 2}, at::kByte, dev);
-  Tensor scales = make({static_cast<int64_t>(nsc)}, at::kByte, dev);
-  OptTensor g, tc, ts;
+  const int64_t sc = static_cast<int64_t>(nsc), st = static_cast<int64_t>(tsc);
+  const int64_t wsb = workspace ? 0 : static_cast<int64_t>(L.weight_workspace());
+  Bytes b(Bytes::room(n * (k / 2)) + Bytes::room(sc) + wsb, dev);
+  const Tensor codes = b.take({n, k / 2}), scales = b.take({sc});
+  OptTensor g, tc, ts, ws = workspace;
+  if (!ws) ws = b.take({wsb});
   if (fmt == QLORA_FP4_NV) g = make({1}, at::kFloat, dev);
-  if (transposed) {
-    tc = make({k, n / 2}, at::kByte, dev);
-    ts = make({static_cast<int64_t>(tsc)}, at::kByte, dev);
+  if (transposed) {  // an allocation of its own: it may be dropped by itself
+    Bytes t(Bytes::room(k * (n / 2)) + st, dev);
+    tc = t.take({k, n / 2});
+    ts = t.take({st});
   }
-  weight_out(W, fmt, codes, scales, g, tc, ts, workspace);
+  weight_out(W, fmt, codes, scales, g, tc, ts, ws);
   return py::make_tuple(codes, scales, g, tc, ts);
 }
 
