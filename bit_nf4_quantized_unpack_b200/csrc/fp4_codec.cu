@@ -826,8 +826,12 @@ template <bool BF16>
 cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format, uint8_t* codes,
                           uint8_t* scales, float* gscale, cudaStream_t st) {
   if (format == QLORA_FP4_MX) {
+    // bf16: two segments a warp where that leaves eight CTAs for each SM (8192 x 11008: 38.3 us
+    // against 39.8; 1000 x 4096: 3.8 against 3.2); fp32 is 2 % slower so
+    const int64_t segs = (cols + 511) / 512, half = (segs + 1) / 2;
+    const bool two = BF16 && (rows + 7) / 8 * half >= 8 * static_cast<int64_t>(num_sms());
     const dim3 grid(static_cast<unsigned>((rows + 7) / 8),
-                    static_cast<unsigned>(std::min((cols + 511) / 512, kMaxGridY)));
+                    static_cast<unsigned>(std::min(two ? half : segs, kMaxGridY)));
     return launch_pdl(k_fp4_quantize_mx<BF16>, grid, dim3(256), 0, st, X,
                       static_cast<uint32_t>(rows), cols, codes, scales);
   }
