@@ -567,6 +567,10 @@ struct LoraArgs {
   int tiles0;        // row tiles of the first problem; later tiles belong to the second
   float* partial;    // [splits][rows_pad][64] fp32 (NC > 64: the parts' columns summed)
   int64_t rows_pad;  // the problems' row tiles stacked: 128 x (tiles0 + tiles of the second)
+  // The stream's previous kernel writes nothing that this one reads or writes, and has itself
+  // waited for all before it before it let this one start: run beside it, and wait for it
+  // at the end (who waits for this kernel has then waited for that one).
+  bool beside;
   int* err;
 };
 
@@ -623,7 +627,8 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
-  griddep_wait_and_release();
+  if (args.beside) griddep_release();
+  else griddep_wait_and_release();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -730,6 +735,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_d, lora_tmem(NC));
   }
+  if (args.beside) griddep_wait();
 }
 
 // ================================================================== finalize kernels
@@ -946,7 +952,7 @@ template <bool A_MN, bool B_MN, int NC>
 cudaError_t run_lora_gemm(const CUtensorMap& ta, const CUtensorMap& tb, int64_t rows0,
                           int64_t contraction, float* partial, cudaStream_t st, int* splits_out,
                           const CUtensorMap* ta1 = nullptr, const CUtensorMap* tb1 = nullptr,
-                          int64_t rows1 = 0) {
+                          int64_t rows1 = 0, bool beside = false) {
   const int64_t rows = ta1 ? stacked_rows(rows0, rows1) : rows0;
   const SplitPlan p = plan_split(rows, contraction);
   LoraArgs a;
@@ -955,6 +961,7 @@ cudaError_t run_lora_gemm(const CUtensorMap& ta, const CUtensorMap& tb, int64_t 
   a.steps_per = p.steps_per;
   a.partial = partial;
   a.rows_pad = p.rows_pad;
+  a.beside = beside;
   a.err = device_error_word();
   auto kern = k_lora_gemm<A_MN, B_MN, NC>;
   const uint32_t smem = lora_smem(NC);
@@ -1298,32 +1305,33 @@ qlora_status gemm_shard_bwd(const uint16_t* dY, const uint16_t* X, const float* 
 // ---- the linear layer on a microscaled 4-bit weight: the same rank-r products, with the
 // 16-bit X and dY; only the large product sees their 4-bit form.
 namespace {
-// first(st), and second() on the side stream: `st` continues once both are done. Without it (not
-// wanted, or not there) second, then first: the quantizer reads rows that are not in L2 faster
-// than the rank-r product does.
-template <typename First, typename Second>
-cudaError_t beside(cudaStream_t st, bool wanted, First&& first, Second&& second) {
+// Quantizing (unless `quantize` is false) beside the rank-r product that reads the same rows; NVFP4,
+// N = K = 4096, r = 64. From kSideM tokens the quantizer fills the SMs: the product runs first,
+// the quantizer on the side stream (4096 tokens, in a graph: forward 49.9 us, in order 53.4;
+// backward 73.6, 76.8). Below, events between streams cost an eager call more than the
+// overlap gives (512 tokens, backward: 35.1 us, in order 33.0). There the product is told
+// (`true`) that it may start behind the quantizer without waiting for it (512 tokens,
+// forward: 20.7 us, waiting 22.8).
+constexpr int64_t kSideM = 1024;
+template <typename Quantizer, typename Product>
+cudaError_t quantize_and_rank(cudaStream_t st, int64_t M, bool quantize, Quantizer&& quantizer, Product&& product) {
+  if (!quantize) return product(st, false);
   SideStream* side = nullptr;
-  cudaError_t e = wanted ? side_stream(st, &side) : cudaSuccess;
+  cudaError_t e = M >= kSideM ? side_stream(st, &side) : cudaSuccess;
   if (e != cudaSuccess) return e;
   if (!side) {
-    e = second(st);
-    return e == cudaSuccess ? first(st) : e;
+    e = quantizer(st);
+    return e == cudaSuccess ? product(st, true) : e;
   }
   e = cudaEventRecord(side->fork, st);
   if (e == cudaSuccess) e = cudaStreamWaitEvent(side->st, side->fork, 0);
   if (e != cudaSuccess) return e;
-  e = first(st);
-  if (e == cudaSuccess) e = second(side->st);
+  e = product(st, false);
+  if (e == cudaSuccess) e = quantizer(side->st);
   cudaError_t ej = cudaEventRecord(side->join, side->st);  // on every path
   if (ej == cudaSuccess) ej = cudaStreamWaitEvent(st, side->join, 0);
   return e == cudaSuccess ? ej : e;
 }
-// From here on quantizing runs beside the rank-r product that reads the same rows (NVFP4, N = K =
-// 4096, r = 64, in a graph: 4096 tokens 49.9 us forward and 73.6 backward, one after the other 53.4
-// and 76.8). Below, the events cost an eager call as much or more (512 tokens, backward:
-// 35.1 us against 33.0; 1024 tokens: 36.9 against 37.6).
-constexpr int64_t kBesideM = 1024;
 
 qlora_fp4_matrix carve_fp4(Carve& c, int64_t rows, int64_t cols, int format, Fp4Out* out) {
   out->codes = c.take<uint8_t>(static_cast<size_t>(rows) * (cols / 2));
@@ -1424,10 +1432,12 @@ qlora_status fp4_forward(const uint16_t* X, const qlora_fp4_matrix& w, const uin
   QL_MAP(&ta, kBF16, X, s.K, s.M, s.K * 2, 64, 128, kSW128);   // X K-major
   QL_MAP(&tb, kBF16, A, s.r, s.K, s.r * 2, 64, 64, kSW128);    // A as MN-major (j inner)
   int splits = 0;
-  QL_TRY(beside(
-      st, s.M >= kBesideM,
-      [&](cudaStream_t on) { return run_lora_gemm<false, true, 64>(ta, tb, s.M, s.K, part, on, &splits); },
-      [&](cudaStream_t on) { return launch_fp4_quantize(X, true, s.M, s.K, w.format, xo, on); }));
+  QL_TRY(quantize_and_rank(
+      st, s.M, true,
+      [&](cudaStream_t on) { return launch_fp4_quantize(X, true, s.M, s.K, w.format, xo, on); },
+      [&](cudaStream_t on, bool beside) {
+        return run_lora_gemm<false, true, 64>(ta, tb, s.M, s.K, part, on, &splits, nullptr, nullptr, 0, beside);
+      }));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                     splits, plan_split(s.M, s.K).rows_pad, s.M, s.r, s.scale, T_save, ts, nullptr,
                     nullptr, nullptr, x.gscale, w.gscale, 2));
@@ -1454,11 +1464,11 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   int splits = 0;
   QL_MAP(&ta, kBF16, dY, s.N, s.M, s.N * 2, 64, 128, kSW128);  // dY K-major (over n)
   QL_MAP(&tb, kBF16, B, s.N, s.r, s.N * 2, 64, 64, kSW128);    // B [r, N] K-major
-  QL_TRY(beside(
-      st, dX && s.M >= kBesideM,
-      [&](cudaStream_t on) { return run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, on, &splits); },
-      [&](cudaStream_t on) {
-        return dX ? launch_fp4_quantize(dY, true, s.M, s.N, wt.format, b.yo, on) : cudaSuccess;
+  QL_TRY(quantize_and_rank(
+      st, s.M, dX != nullptr,
+      [&](cudaStream_t on) { return launch_fp4_quantize(dY, true, s.M, s.N, wt.format, b.yo, on); },
+      [&](cudaStream_t on, bool) {  // started without waiting it gained nothing here (29.8 us, 29.0)
+        return run_lora_gemm<false, false, 64>(ta, tb, s.M, s.N, part, on, &splits);
       }));
   QL_TRY(launch_pdl(k_finalize_rank, dim3(blocks_for(s.M * 64, 256)), dim3(256), 0, st, part,
                     splits, plan_split(s.M, s.N).rows_pad, s.M, s.r, s.scale, nullptr, b.gs, b.g3, t,
@@ -1467,7 +1477,8 @@ qlora_status fp4_backward(const uint16_t* dY, const uint16_t* X, const float* T_
   QL_MAP(&gb, kBF16, b.g3, 192, s.M, 384, 64, 64, kSW128);       // G in three parts, MN-major
   QL_MAP(&ga1, kBF16, dY, s.N, s.M, s.N * 2, 64, 64, kSW128);  // dY as MN-major (n inner)
   QL_MAP(&gb1, kBF16, b.t3, 192, s.M, 384, 64, 64, kSW128);      // T in three parts, MN-major
-  // dA and dB beside dX, as in gemm_backward
+  // dA and dB beside dX, as in gemm_backward (started behind dX's product on the same stream
+  // without waiting for it, their sums came after it: 2-3 us more at 200 to 300 tokens)
   SideStream* side = nullptr;
   if (dX) QL_TRY(side_stream(st, &side));
   cudaStream_t gst = st;

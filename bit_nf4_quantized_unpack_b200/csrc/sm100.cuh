@@ -331,9 +331,13 @@ __device__ __forceinline__ uint32_t sw128_kmajor_offset(uint32_t row, uint32_t c
 // kernel of the stream still runs: they set up shared memory and TMEM, then wait here for
 // that kernel (and so, transitively, every earlier one) to complete before touching
 // global memory, and let their own dependents start launching.
-__device__ __forceinline__ void griddep_wait_and_release() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void griddep_wait_and_release() {
+  griddep_wait();
+  griddep_release();
 }
 
 // ---------------------------------------------------------------- thread-block clusters

@@ -368,6 +368,31 @@ def test_large_batch_on_streams_and_in_graphs(fmt):
             assert all(torch.equal(x, y) for x, y in zip(out, ref))
 
 
+@pytest.mark.parametrize("M", [2, 150, 700, 1100])
+def test_calls_back_to_back_on_one_buffer(M):
+    """Kernels of a call start before their predecessors end: the input rewritten between calls
+    without a synchronisation, the workspace and the outputs' memory reused by every call."""
+    W, A, B, X, dY = (t.cuda() for t in layer(17, M, 512, 1024, 16, 1))
+    q = qlora.qlora_fp4_quantize_weight(W)
+    xs = [X, X.flip(0).contiguous(), (X * 3).contiguous()]
+    ws = torch.empty(max(qlora.qlora_fp4_linear_fwd_workspace_size(M, 512, 1024, 16),
+                         qlora.qlora_fp4_linear_bwd_workspace_size(M, 512, 1024, 16)),
+                     dtype=torch.uint8, device="cuda")
+    want = []
+    for x in xs:
+        y, t = qlora.qlora_fp4_linear_fwd(x, q, A, B, 0.5)
+        want.append((y, t) + qlora.qlora_fp4_linear_bwd(dY, x, t, q, A, B, 0.5))
+        torch.cuda.synchronize()
+    buf, got = torch.empty_like(X), []
+    for i in range(30):
+        buf.copy_(xs[i % 3])
+        y, t = qlora.qlora_fp4_linear_fwd(buf, q, A, B, 0.5, workspace=ws)
+        got.append((y, t) + qlora.qlora_fp4_linear_bwd(dY, buf, t, q, A, B, 0.5, workspace=ws))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i % 3])), i
+
+
 def test_training_step_on_a_microscaled_weight():
     """The operators together: lay the weight out, forward, backward, optimizer step, and the
     next forward on the updated adapter."""
