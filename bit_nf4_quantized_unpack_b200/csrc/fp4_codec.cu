@@ -6,11 +6,11 @@
 //   largest magnitude of the row (activations) or of the matrix (weights); g = 1 for top = 0;
 //   scale byte c = e4m3(amax / g / 6), code = e2m1(x / g / c), 0 where c = 0.
 // e2m1() and e4m3() round to nearest, ties to even, and saturate. With g a power of two the
-// only inexact steps are those roundings: x / g is exact, and the fp32 quotients amax / 6 and
-// x / c are correctly rounded and land on a rounding border only when the real quotient does
-// (numerator and border times divisor are both fp32 numbers, so a real quotient off the border
-// is off by more than half an fp32 ulp). Codes and scales are therefore those of the
-// definition in real arithmetic.
+// only inexact steps are those roundings: x / g is exact, the fp32 quotient amax / 6 is correctly
+// rounded, x / (g c) is the rounding of a number within 2^-20 ulp of the real quotient, and
+// either lands on a rounding border only when the real quotient does (numerator and border
+// times divisor are both fp32 numbers, so a real quotient off the border is off by more than
+// half an fp32 ulp). Codes and scales are therefore those of the definition in real arithmetic.
 // A block that holds a NaN or an infinity gets the NaN scale and zero codes; its non-finite
 // values do not enter top.
 #include <cuda_bf16.h>
