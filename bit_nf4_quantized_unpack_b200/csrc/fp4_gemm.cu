@@ -616,7 +616,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       };
       auto emit = [&](int j, const uint32_t (&v)[32]) {
         const int64_t q = t.q0 + cs[j] * 32;
-        if (q >= args.Q) return;
+        // Nothing to store: the stage buffers are left alone and not counted, since the waits below
+        // count on a bulk group for every use of a buffer.
+        if (q >= args.Q || p0 >= args.P) return;
         if constexpr (OUT_F32) {
           // the chunk fills both stage buffers: stage[token][row]
           const uint32_t st = smem_u32(stage2);
@@ -655,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (p0 < args.P && elect_one()) {
+        if (elect_one()) {
           tma_store_2d(&tm_out, OUT_F32 ? stage2 : stage2 + (chunks & 1) * 2048, static_cast<int>(p0),
                        static_cast<int>(q));
           bulk_commit_group();

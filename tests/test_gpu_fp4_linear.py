@@ -89,6 +89,28 @@ def test_matmul_schedules(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [
+    (20000, 288, 32),      # wide tiles, every second one with 32 rows of the weight
+    (9000, 928, 32),       # the last of four with 160
+    (20000, 1152, 64),     # the last of five in one CTA of the pair
+    (5000, 4128, 32),
+    (300, 12320, 32),      # narrow tiles
+])
+def test_matmul_tiles_past_the_last_weight_row(M, N, K, fmt):
+    """Many tiles a CTA pair, some of whose warps have no weight row: the rows that such a warp
+    finished before stay as they are. Both epilogues scale the same fp32 sums in the same order, so the
+    bf16 output is the fp32 one rounded."""
+    a, b = normal(M + K, M, K).cuda(), normal(N, N, K, std=0.02).cuda()
+    qa, qb = qlora.qlora_fp4_quantize(a, fmt), qlora.qlora_fp4_quantize(b, fmt)
+    got = qlora.qlora_fp4_matmul(qa, qb, torch.float32)
+    for _ in range(10):
+        assert torch.equal(qlora.qlora_fp4_matmul(qa, qb), got.to(torch.bfloat16))
+    va, vb = (qlora.qlora_fp4_dequant(q, torch.float32).double() for q in (qa, qb))
+    want, mag = va @ vb.t(), va.abs() @ vb.abs().t()
+    assert ((got.double() - want).abs() <= (K / 64 + 8) * U * mag).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_matmul_reads_every_scale_in_its_place(fmt):
     """One-hot codes under scales that all differ: each output is one product of a code and two
     scales, exact in fp32."""
