@@ -13,6 +13,10 @@
 // half an fp32 ulp). Codes and scales are therefore those of the definition in real arithmetic.
 // A block that holds a NaN or an infinity gets the NaN scale and zero codes; its non-finite
 // values do not enter top.
+//
+// Inputs are read by plain loads through pointers that are not __restrict__: they may have been
+// written by a kernel that was still running when this one began, which rules out the read-only
+// path (__ldg), and nothing may be loaded ahead of griddep_wait_and_release.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -40,7 +44,7 @@ struct Raw16<true> {
   uint32_t w[8];
   __device__ __forceinline__ void load(const void* base, int64_t elem) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem);
-    const uint4 a = __ldg(p), b = __ldg(p + 1);
+    const uint4 a = p[0], b = p[1];
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
   }
   __device__ __forceinline__ void zero() {
@@ -68,7 +72,7 @@ struct Raw16<false> {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + elem);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 q = __ldg(p + i);
+      const float4 q = p[i];
       v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
     }
   }
@@ -202,7 +206,7 @@ __device__ __forceinline__ uint32_t gather4(uint32_t sb) {
 // whose scale bytes share sectors.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    k_fp4_quantize_mx(const void* __restrict__ X, uint32_t rows, int64_t cols,
+    k_fp4_quantize_mx(const void* X, uint32_t rows, int64_t cols,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   griddep_wait_and_release();
   const int lane = threadIdx.x & 31;
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(256)
 // U = 0: rows too long for that are read twice.
 template <bool BF16, int U>
 __global__ void __launch_bounds__(512)
-    k_fp4_quantize_nv(const void* __restrict__ X, uint32_t rows, int64_t cols,
+    k_fp4_quantize_nv(const void* X, uint32_t rows, int64_t cols,
                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                       float* __restrict__ gscale) {
   griddep_wait_and_release();
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(512)
 // One row by a CTA of 256 threads, in passes of four chunks a thread; a row that fits one pass
 // stays in registers between the maximum and the codes.
 template <Fp4 F>
-__device__ __forceinline__ void quantize_row(const uint16_t* __restrict__ X, int64_t row, int64_t cols,
+__device__ __forceinline__ void quantize_row(const uint16_t* X, int64_t row, int64_t cols,
                                              uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                              float* __restrict__ gscale, uint32_t* part) {
   constexpr int U = 4, NT = 256;
@@ -402,9 +406,9 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 
 template <Fp4 F, bool A_T>
 __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kPrepThreads)
-    k_fp4_prep(const uint16_t* __restrict__ X, int M, int64_t K, uint8_t* __restrict__ codes,
+    k_fp4_prep(const uint16_t* X, int M, int64_t K, uint8_t* __restrict__ codes,
                uint8_t* __restrict__ scales, float* __restrict__ gscale, int row_ctas,
-               const uint16_t* __restrict__ A, int r, float* __restrict__ T) {
+               const uint16_t* A, int r, float* __restrict__ T) {
   griddep_wait_and_release();
   __shared__ uint32_t part[16];
   __shared__ __align__(16) uint8_t xs[kPrepTok * kPrepXPitch];
@@ -487,8 +491,8 @@ static_assert(kPrepTok * kPrepCols == kPrepThreads && 8 * 256 * 4 <= kPrepTok * 
 // was bound by shared memory (12 us for r = 64, K = N = 4096).
 constexpr int kGradCols = 64, kGradTok = 32, kGradPitch = 64 * 2 + 16;
 __global__ void __launch_bounds__(256)
-    k_fp4_small_grads(const uint16_t* __restrict__ X, const uint16_t* __restrict__ dY, int M, int64_t K,
-                      int64_t N, const float* __restrict__ G, int g_parts, const float* __restrict__ T,
+    k_fp4_small_grads(const uint16_t* X, const uint16_t* dY, int M, int64_t K,
+                      int64_t N, const float* G, int g_parts, const float* T,
                       int t_parts, int r, float scale, float* __restrict__ dA, float* __restrict__ dB) {
   griddep_wait_and_release();
   __shared__ __align__(16) uint8_t xs[kGradTok * kGradPitch], vs[3][kGradTok * kGradPitch];
@@ -505,14 +509,14 @@ __global__ void __launch_bounds__(256)
   auto fetch = [&](int m0) {
     const bool in = m0 + lt < M;
     w = make_uint4(0u, 0u, 0u, 0u);
-    if (in && c0 + lc < C) w = __ldg(reinterpret_cast<const uint4*>(src + (m0 + lt) * C + c0 + lc));
+    if (in && c0 + lc < C) w = *reinterpret_cast<const uint4*>(src + (m0 + lt) * C + c0 + lc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
     if (in && lc < r) {
       const float* p = val + static_cast<int64_t>(m0 + lt) * r + lc;
 #pragma unroll 2
       for (int i = 0; i < parts; ++i, p += static_cast<int64_t>(M) * r) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
       }
@@ -581,7 +585,7 @@ template <bool BF16>
 constexpr int kAmaxChunks = BF16 ? 4 : 2;  // per thread, all in flight: 128 bytes
 template <bool BF16>
 __global__ void __launch_bounds__(kAmaxThreads)
-    k_fp4_amax(const void* __restrict__ W, int64_t chunks, uint32_t* __restrict__ parts) {
+    k_fp4_amax(const void* W, int64_t chunks, uint32_t* __restrict__ parts) {
   griddep_wait_and_release();
   __shared__ uint32_t part[32];
   uint32_t m = 0u;
@@ -631,7 +635,7 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
 // transposed copy has the same squares, so it stores the same values.
 template <Fp4 F, bool BF16>
 __global__ void __launch_bounds__(32)
-    k_fp4_quantize_weight(const void* __restrict__ W, int64_t n, int64_t k,
+    k_fp4_quantize_weight(const void* W, int64_t n, int64_t k,
                           const uint32_t* tops, int ntops, uint8_t* __restrict__ codes,
                           uint8_t* __restrict__ scales, float* __restrict__ gscale,
                           uint8_t* __restrict__ t_codes, uint8_t* __restrict__ t_scales) {
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(32)
   Gscale g(0);
   if (F == Fp4::kNv) {
     uint32_t top = 0u;
-    for (int i = lane; i < ntops; i += 32) top = max(top, __ldg(tops + i));
+    for (int i = lane; i < ntops; i += 32) top = max(top, tops[i]);
     g = Gscale(nv_gscale_exp(__reduce_max_sync(~0u, top)));
     if (blockIdx.x == 0 && blockIdx.y == 0 && lane == 0) *gscale = g.g;
   }
@@ -659,13 +663,13 @@ __global__ void __launch_bounds__(32)
   for (int i = 0; i < 8; ++i) {
     if constexpr (BF16) {
       rb[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (in) rb[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + (gn + i) * k + gk));
+      if (in) rb[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + (gn + i) * k + gk);
     } else {
       rf[2 * i] = rf[2 * i + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (in) {
         const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(W) + (gn + i) * k + gk);
-        rf[2 * i] = __ldg(p);
-        rf[2 * i + 1] = __ldg(p + 1);
+        rf[2 * i] = p[0];
+        rf[2 * i + 1] = p[1];
       }
     }
   }
@@ -771,8 +775,8 @@ __global__ void __launch_bounds__(32)
 // mantissa bits), then one rounding to bf16 where asked.
 template <Fp4 F, bool BF16>
 __global__ void __launch_bounds__(256)
-    k_fp4_dequant(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                  const float* __restrict__ gscale, bool g_per_row, uint32_t rows, int64_t cols,
+    k_fp4_dequant(const uint8_t* codes, const uint8_t* scales,
+                  const float* gscale, bool g_per_row, uint32_t rows, int64_t cols,
                   int64_t ktiles, void* __restrict__ out) {
   griddep_wait_and_release();
   constexpr int V = BF16 ? 8 : 4;          // values per lane and stride
@@ -780,7 +784,7 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const uint32_t row = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const float g = gscale ? __ldg(gscale + (g_per_row ? row : 0)) : 1.f;
+  const float g = gscale ? gscale[g_per_row ? row : 0] : 1.f;
   const uint64_t g2 = f2_pack(g, g);
   for (int64_t c0 = static_cast<int64_t>(blockIdx.y) * 1024; c0 < cols; c0 += static_cast<int64_t>(gridDim.y) * 1024) {
     uint32_t w[U], sb[U];
@@ -790,9 +794,8 @@ __global__ void __launch_bounds__(256)
       w[u] = sb[u] = 0u;
       if (col < cols) {
         const uint8_t* src = codes + (row * cols + col) / 2;
-        w[u] = BF16 ? __ldg(reinterpret_cast<const uint32_t*>(src))
-                    : __ldg(reinterpret_cast<const uint16_t*>(src));
-        sb[u] = __ldg(scales + fp4_scale_offset(row, col / kFp4Block<F>, ktiles));
+        w[u] = BF16 ? *reinterpret_cast<const uint32_t*>(src) : *reinterpret_cast<const uint16_t*>(src);
+        sb[u] = scales[fp4_scale_offset(row, col / kFp4Block<F>, ktiles)];
       }
     }
 #pragma unroll

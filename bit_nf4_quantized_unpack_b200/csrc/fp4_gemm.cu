@@ -5,6 +5,9 @@
 // a: tokens, b: weight rows, both E2M1 codes with block scales along k; tcgen05.mma
 // kind::mxf4nvf4 multiplies codes and scales and adds in fp32. The weight is the 128-lane
 // operand, tokens are the columns of the accumulator.
+//
+// gscales and T may have been written by a kernel that was still running when this one began:
+// plain loads behind griddep_wait, never the read-only path (__ldg).
 #include <algorithm>
 
 #include "fp4_device.cuh"
@@ -239,12 +242,12 @@ __global__ void __launch_bounds__(kSplitThreads)
         const int q = i >> 3, j = (i & 7) * 8;
         float v[8] = {};
         if (q < Q && j < sa.r) {
-          const float ia = args.gq ? 1.f / __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
+          const float ia = args.gq ? 1.f / args.gq[args.gq_rows ? q : 0] : 1.f;
 #pragma unroll 4
           for (int part = 0; part < sa.t_parts; ++part) {
             const float4* src =
                 reinterpret_cast<const float4*>(sa.t + (static_cast<int64_t>(part) * Q + q) * sa.r + j);
-            const float4 x = __ldg(src), y = __ldg(src + 1);
+            const float4 x = src[0], y = src[1];
             v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
             v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
           }
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     float g4[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      g4[j] = args.gp ? __ldg(args.gp + (args.gp_rows ? min(p4 + j, args.P - 1) : 0)) : 1.f;
+      g4[j] = args.gp ? args.gp[args.gp_rows ? min(p4 + j, args.P - 1) : 0] : 1.f;
     const bool got = mbar_wait(acc_full, 0, abort_flag) && !*abort_flag;
     if (!got && !*abort_flag) record_error(args.err, abort_flag, kErrTimeoutEpilogue);
     tc_fence_after();
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         for (int i = 0; i < kAt; ++i) {
           const int q = q0 + 4 * i;
           if (q >= t1 || p4 >= args.P) continue;  // P is a multiple of 8
-          const float gq = args.gq ? __ldg(args.gq + (args.gq_rows ? q : 0)) : 1.f;
+          const float gq = args.gq ? args.gq[args.gq_rows ? q : 0] : 1.f;
           const float4 o = make_float4(sum[i].x * g4[0] * gq, sum[i].y * g4[1] * gq,
                                        sum[i].z * g4[2] * gq, sum[i].w * g4[3] * gq);
           if (args.out_f32)
@@ -591,10 +594,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int j = 0; j < 4; ++j) {
         gq[j] = 1.f;
         gp[j] = 1.f;
-        if (args.gq && j < kChunks) gq[j] = __ldg(args.gq + (args.gq_rows ? min(t.q0 + cs[j] * 32 + lane, args.Q - 1) : 0));
+        if (args.gq && j < kChunks) gq[j] = args.gq[args.gq_rows ? min(t.q0 + cs[j] * 32 + lane, args.Q - 1) : 0];
         // rows lane / 4 + 8 j of the quarter (bf16 output), row lane (fp32 output, j = 0)
         const int64_t row = p0 + (OUT_F32 ? lane : (lane >> 2) + 8 * j);
-        if (args.gp) gp[j] = __ldg(args.gp + (args.gp_rows ? min(row, args.P - 1) : 0));
+        if (args.gp) gp[j] = args.gp[args.gp_rows ? min(row, args.P - 1) : 0];
       }
       if (!mbar_wait(&acc_full[i & 1], (i >> 1) & 1u, abort_flag)) {
         if (!*abort_flag) record_error(args.err, abort_flag, kErrTimeoutEpilogue);

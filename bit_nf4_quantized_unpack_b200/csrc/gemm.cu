@@ -756,12 +756,13 @@ __device__ __forceinline__ void store_parts(uint16_t* __restrict__ out, int64_t 
 //   With t_in, also the bf16 parts of that fp32 [M, r] (into t_hilo).
 //   With ga (one per row) and gb (one), scale * v is divided by both first: the operand of
 //   a product whose accumulator is multiplied by them at the end.
-__global__ void k_finalize_rank(const float* __restrict__ part, int splits, int64_t rows_pad,
+// (Inputs are not __restrict__: the kernel that writes them may still run when this one begins, so
+// they must not go through the read-only path.)
+__global__ void k_finalize_rank(const float* part, int splits, int64_t rows_pad,
                                 int64_t M, int r, float scale, float* __restrict__ plain,
                                 uint16_t* __restrict__ scaled, uint16_t* __restrict__ hilo,
-                                const float* __restrict__ t_in, uint16_t* __restrict__ t_hilo,
-                                const float* __restrict__ ga, const float* __restrict__ gb,
-                                int parts) {
+                                const float* t_in, uint16_t* __restrict__ t_hilo, const float* ga,
+                                const float* gb, int parts) {
   griddep_wait_and_release();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (i >= M * 64) return;
@@ -809,7 +810,7 @@ __global__ void k_finalize_rank(const float* __restrict__ part, int splits, int6
 constexpr int kGradRows = 16;
 static_assert(128 % kGradRows == 0, "a block of rows never straddles the two problems");
 __global__ void __launch_bounds__(256)
-    k_finalize_grad(const float* __restrict__ part, int splits, int64_t rows_pad, int64_t pad0,
+    k_finalize_grad(const float* part, int splits, int64_t rows_pad, int64_t pad0,
                     int64_t rows0, float* __restrict__ out0, int64_t rows1,
                     float* __restrict__ out1, int r, float scale) {
   griddep_wait_and_release();
