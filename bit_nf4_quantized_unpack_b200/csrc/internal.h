@@ -57,8 +57,17 @@ void note_launches(int n);                         // count kernels enqueued (ql
 
 // ---- launch, workspace and error helpers ------------------------------------------
 // Launch on `st` with programmatic stream serialization: the kernel may begin (its
-// prologue) while the stream's previous kernel drains; every kernel launched this
-// way waits for its predecessor with griddep_wait_and_release before it touches global memory.
+// prologue) while the stream's previous kernel drains. Every kernel launched this way waits for
+// its predecessor and only then lets its successor start (griddep_wait_and_release), before it
+// touches global memory, with two exceptions:
+//   k_lora_gemm with `beside` lets its successor start, works, and waits at its end;
+//   k_fp4_gemm_split with `early` fetches weight tiles, their scales and the rank-r operand of the
+//   weight's side before it waits.
+// Both are sound only directly behind a kernel that keeps the rule (so that everything before that one has
+// completed) and that writes none of what they touch before their wait: launch_fp4_quantize and
+// launch_fp4_prep. Nothing may be launched between, and those kernels keep
+// griddep_wait_and_release as their first statement. A kernel that starts without waiting has to
+// wait before it ends, since who waits for it counts on all before it.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t st, Args&&... args) {
@@ -152,6 +161,7 @@ int64_t fp4_ktiles(int64_t cols, int format);  // scale tiles along a row
 inline size_t fp4_scales_bytes(int64_t rows, int64_t cols, int format) {
   return static_cast<size_t>((rows + 127) / 128) * fp4_ktiles(cols, format) * 512;
 }
+// Its kernels wait, then release, first of all: a `beside` launch may follow (see launch_pdl).
 cudaError_t launch_fp4_quantize(const void* X, bool bf16, int64_t rows, int64_t cols, int format,
                                 const Fp4Out& out, cudaStream_t st);
 // ws: room for kFp4MaxTops words.
@@ -161,7 +171,8 @@ cudaError_t launch_fp4_quantize_weight(const void* W, bool bf16, int64_t n, int6
                                        cudaStream_t st);
 cudaError_t launch_fp4_dequant(const qlora_fp4_matrix& q, bool bf16, void* out, cudaStream_t st);
 // Few tokens: quantizes X [M, K] bf16 to `out` (unless NULL) and writes the parts over K of
-// T = X A, A [K, r] or (a_t) [r, K], fp32 [fp4_prep_parts(K)][M][r], in one launch.
+// T = X A, A [K, r] or (a_t) [r, K], fp32 [fp4_prep_parts(K)][M][r], in one launch, which waits,
+// then releases, first of all: an `early` product may follow (see launch_pdl).
 int fp4_prep_parts(int64_t K);
 cudaError_t launch_fp4_prep(const uint16_t* X, int64_t M, int64_t K, int format, const Fp4Out* out,
                             const uint16_t* A, bool a_t, int r, float* T, cudaStream_t st);
@@ -184,7 +195,7 @@ struct Fp4Ext {
   bool mn_major;
 };
 constexpr int64_t kFp4SplitMaxM = 128;
-// early: the previous launch on `st` is launch_fp4_prep.
+// early: the previous launch on `st` is launch_fp4_prep, which writes neither b nor ext->p.
 qlora_status fp4_product(const qlora_fp4_matrix& a, const qlora_fp4_matrix& b, const Fp4Ext* ext,
                          void* out, bool out_f32, bool early, cudaStream_t st);
 // The linear layer on a microscaled weight (gemm.cu): w is W [N, K], wt its transposed copy.

@@ -330,7 +330,8 @@ __device__ __forceinline__ uint32_t sw128_kmajor_offset(uint32_t row, uint32_t c
 // Kernels launched with programmatic stream serialization may start while the previous
 // kernel of the stream still runs: they set up shared memory and TMEM, then wait here for
 // that kernel (and so, transitively, every earlier one) to complete before touching
-// global memory, and let their own dependents start launching.
+// global memory, and let their own dependents start launching. (launch_pdl names the two kernels
+// that touch global memory before they wait, and what makes that sound.)
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
