@@ -61,9 +61,10 @@ void note_launches(int n);                         // count kernels enqueued (ql
 // its predecessor and only then lets its successor start (griddep_wait_and_release), before it
 // touches global memory, with two exceptions:
 //   k_lora_gemm with `beside` lets its successor start, works, and waits at its end;
-//   k_fp4_gemm_split with `early` fetches weight tiles, their scales and the rank-r operand of the
-//   weight's side before it waits.
-// Both are sound only directly behind a kernel that keeps the rule (so that everything before that one has
+//   k_fp4_gemm_split with `early` (launched by run_split, as it needs a cluster size too) fetches
+//   weight tiles, their scales and the rank-r operand of the weight's side before it waits.
+// (The kernels of codec.cu and decode.cu have launches of their own and release before they wait.)
+// The two exceptions are sound only directly behind a kernel that keeps the rule (so that everything before that one has
 // completed) and that writes none of what they touch before their wait: launch_fp4_quantize and
 // launch_fp4_prep. Nothing may be launched between, and those kernels keep
 // griddep_wait_and_release as their first statement. A kernel that starts without waiting has to
