@@ -487,7 +487,9 @@ static_assert(kPrepTok * kPrepCols == kPrepThreads && 8 * 256 * 4 <= kPrepTok * 
 // Few tokens: dA [K, r] = scale X^T G and dB [r, N] = scale T^T dY, G and T fp32 in parts
 // [parts][M][r]. A CTA takes 64 columns of X (or of dY) and all of the rank, in passes of 32
 // tokens whose successors are fetched meanwhile; a warp 16 x 32 outputs with mma.sync, G (T)
-// as three bf16 parts, which hold an fp32 value to its last bit. At 128 tokens an FMA version
+// as three bf16 parts, which hold an fp32 value to its last bit. The first part has sums of its
+// own: where one is not finite it is the result, since it has the infinities with their signs, while a
+// lower part may be 0 times an infinity or have the other sign. At 128 tokens an FMA version
 // was bound by shared memory (12 us for r = 64, K = N = 4096).
 constexpr int kGradCols = 64, kGradTok = 32, kGradPitch = 64 * 2 + 16;
 __global__ void __launch_bounds__(256)
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(256)
   const int wc = (warp & 3) * 16, wj = (warp >> 2) * 32;  // this warp's outputs
   const uint32_t xa = smem_u32(xs) + (((lane >> 4) * 8 + (lane & 7)) * kGradPitch + (wc + ((lane >> 3) & 1) * 8) * 2);
   const uint32_t va = smem_u32(vs[0]) + ((lane & 15) * kGradPitch + (wj + (lane >> 4) * 8) * 2);
-  float acc[4][4] = {};
+  float acc[4][4] = {}, low[4][4] = {};  // of the first part, of the others
   fetch(0);
   for (int m0 = 0; m0 < M; m0 += kGradTok) {
     __syncthreads();
@@ -554,8 +556,8 @@ __global__ void __launch_bounds__(256)
           for (int h = 0; h < 2; ++h) {
             uint32_t b[4];
             ldmatrix_x4_trans(va + part * (kGradTok * kGradPitch) + t * kGradPitch + h * 32, b);
-            mma_16816(acc[2 * h], a, b[0], b[1]);
-            mma_16816(acc[2 * h + 1], a, b[2], b[3]);
+            mma_16816(part ? low[2 * h] : acc[2 * h], a, b[0], b[1]);
+            mma_16816(part ? low[2 * h + 1] : acc[2 * h + 1], a, b[2], b[3]);
           }
       }
     }
@@ -567,11 +569,13 @@ __global__ void __launch_bounds__(256)
       const int64_t c = c0 + wc + (lane >> 2) + 4 * e;  // rows lane / 4 and, for e = 2, eight on
       const int j = wj + i * 8 + (lane & 3) * 2;
       if (c >= C || j >= r) continue;
+      const float s0 = scale * (isfinite(acc[i][e]) ? acc[i][e] + low[i][e] : acc[i][e]);
+      const float s1 = scale * (isfinite(acc[i][e + 1]) ? acc[i][e + 1] + low[i][e + 1] : acc[i][e + 1]);
       if (!second) {
-        *reinterpret_cast<float2*>(dA + c * r + j) = make_float2(scale * acc[i][e], scale * acc[i][e + 1]);
+        *reinterpret_cast<float2*>(dA + c * r + j) = make_float2(s0, s1);
       } else {
-        dB[j * N + c] = scale * acc[i][e];
-        dB[(j + 1) * N + c] = scale * acc[i][e + 1];
+        dB[j * N + c] = s0;
+        dB[(j + 1) * N + c] = s1;
       }
     }
 }

@@ -61,6 +61,13 @@ __device__ __forceinline__ float2 e2m1_pair(uint32_t w) {
   return __half22float2(v);
 }
 
+// What the bf16 pair hi leaves of (a, b), as a bf16 pair: 0 where hi is infinite (or NaN).
+__device__ __forceinline__ uint32_t bf16x2_rest_rn(float a, float b, uint32_t hi) {
+  const float ra = (hi & 0x7F80u) == 0x7F80u ? 0.f : a - __uint_as_float(hi << 16);
+  const float rb = (hi & 0x7F800000u) == 0x7F800000u ? 0.f : b - __uint_as_float(hi & 0xFFFF0000u);
+  return pack_bf16x2_rn(ra, rb);
+}
+
 // fp32 -> E4M3 bits (nearest, ties to even, 448 at most).
 __device__ __forceinline__ uint32_t e4m3_bits(float x) {
   uint16_t d;

@@ -263,8 +263,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           hi[k] = pack_bf16x2_rn(v[2 * k], v[2 * k + 1]);
-          lo[k] = pack_bf16x2_rn(v[2 * k] - __uint_as_float(hi[k] << 16),
-                                 v[2 * k + 1] - __uint_as_float(hi[k] & 0xFFFF0000u));
+          lo[k] = bf16x2_rest_rn(v[2 * k], v[2 * k + 1], hi[k]);
         }
         const uint32_t off = sw128_kmajor_offset(q, i & 7);
         *reinterpret_cast<uint4*>(ext_s + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);

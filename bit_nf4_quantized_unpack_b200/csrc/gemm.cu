@@ -713,9 +713,12 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
             uint32_t w[32];
             tmem_ld_32x32b_x32(taddr + part * 64 + c * 32, w);
             tmem_ld_wait();
+            // A first part that is not finite stands alone: it has the sum's infinities with their
+            // signs, while a lower part may be 0 times an infinity or have the other sign.
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+              if (isfinite(__uint_as_float(v[i])))
+                v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
           }
         } else {
 #pragma unroll
@@ -739,6 +742,11 @@ __global__ void __launch_bounds__(kLoraThreads, 1)
 }
 
 // ================================================================== finalize kernels
+// What the bf16 number hi leaves of v: nothing where hi is infinite (or NaN).
+__device__ __forceinline__ float bf16_rest(float v, uint16_t hi) {
+  return (hi & 0x7F80u) == 0x7F80u ? 0.f : v - __uint_as_float(static_cast<uint32_t>(hi) << 16);
+}
+
 // v as a sum of `parts` bf16 values, the largest first, at column j of each 64-wide part of
 // row m of out [M, 64 parts].
 __device__ __forceinline__ void store_parts(uint16_t* __restrict__ out, int64_t m, int j, float v,
@@ -746,7 +754,7 @@ __device__ __forceinline__ void store_parts(uint16_t* __restrict__ out, int64_t 
   for (int part = 0; part < parts; ++part) {
     const uint16_t hi = bf16_bits_rn(v);
     out[m * (64 * parts) + part * 64 + j] = hi;
-    v -= __uint_as_float(static_cast<uint32_t>(hi) << 16);
+    v = bf16_rest(v, hi);
   }
 }
 
@@ -796,7 +804,7 @@ __global__ void k_finalize_rank(const float* part, int splits, int64_t rows_pad,
     if (gb) sv /= *gb;
     const uint16_t hi = bf16_bits_rn(sv);
     scaled[m * 128 + j] = hi;
-    scaled[m * 128 + 64 + j] = bf16_bits_rn(sv - __uint_as_float(static_cast<uint32_t>(hi) << 16));
+    scaled[m * 128 + 64 + j] = bf16_bits_rn(bf16_rest(sv, hi));
   }
   if (hilo) store_parts(hilo, m, j, v, parts);
   if (t_hilo) store_parts(t_hilo, m, j, (j < r) ? t_in[m * r + j] : 0.f, parts);
@@ -927,7 +935,7 @@ __global__ void k_rank_from_plain(const float* __restrict__ G, const float* __re
   auto hilo = [&](uint16_t* out, float v) {
     const uint16_t hi = bf16_bits_rn(v);
     out[m * 128 + j] = hi;
-    out[m * 128 + 64 + j] = bf16_bits_rn(v - __uint_as_float(static_cast<uint32_t>(hi) << 16));
+    out[m * 128 + 64 + j] = bf16_bits_rn(bf16_rest(v, hi));
   };
   hilo(gs, g * scale);
   hilo(ghl, g);

@@ -64,9 +64,9 @@ void note_launches(int n);                         // count kernels enqueued (ql
 //   k_fp4_gemm_split with `early` (launched by run_split, as it needs a cluster size too) fetches
 //   weight tiles, their scales and the rank-r operand of the weight's side before it waits.
 // (The kernels of codec.cu and decode.cu have launches of their own and release before they wait.)
-// The two exceptions are sound only directly behind a kernel that keeps the rule (so that everything before that one has
-// completed) and that writes none of what they touch before their wait: launch_fp4_quantize and
-// launch_fp4_prep. Nothing may be launched between, and those kernels keep
+// The two exceptions are sound only directly behind a kernel that keeps the rule (so that
+// everything before that one has completed) and that writes none of what they touch before their
+// wait: launch_fp4_quantize and launch_fp4_prep. Nothing may be launched between, and those kernels keep
 // griddep_wait_and_release as their first statement. A kernel that starts without waiting has to
 // wait before it ends, since who waits for it counts on all before it.
 template <typename... KArgs, typename... Args>

@@ -491,6 +491,9 @@ size_t qlora_fp4_linear_fwd_workspace_size(int64_t M, int64_t n_out, int64_t k_i
  * layouts and errors as qlora_linear_fwd. The LoRA term is carried in units of the gscales:
  * a given gscale of w has to be a normal non-zero number, and
  * |scale T| / (gscale of the row * gscale of w) has to stay in bf16's range.
+ * A NaN or an infinity in a row of X makes that row of Y NaN (q() does) and no other. An
+ * infinity in A reaches Y as the formula says; one in B comes out as an infinity or a NaN, as
+ * it meets scale T in two bf16 parts, whose second may be 0 or have the other sign.
  */
 qlora_status qlora_fp4_linear_fwd(const uint16_t *X, int64_t M, qlora_fp4_matrix w,
                                   const uint16_t *A, const uint16_t *B, int r, float scale,
@@ -506,8 +509,10 @@ size_t qlora_fp4_linear_bwd_workspace_size(int64_t M, int64_t n_out, int64_t k_i
  * (straight-through), W frozen:
  *   G = dY B^T,  dX = bf16(q(dY) W + scale G A^T),  dA = scale X^T G,  dB = scale T^T dY
  * wt is W^T [K, N] of qlora_fp4_quantize_weight. q() rounds dY to nearest in blocks along N,
- * for the large product only; G, dA and dB see the 16-bit dY. Other arguments, layouts and
- * errors as qlora_linear_bwd.
+ * for the large product only; G, dA and dB see the 16-bit dY. Infinities reach dA and dB as the
+ * formulas say (a G or T beyond bf16's largest number counts as one). A NaN or an infinity in
+ * a row of dY makes that row of dX NaN and no other; one in A comes out in dX as an infinity or a
+ * NaN. Other arguments, layouts and errors as qlora_linear_bwd.
  */
 qlora_status qlora_fp4_linear_bwd(const uint16_t *dY, const uint16_t *X, const float *T_saved,
                                   int64_t M, qlora_fp4_matrix wt, const uint16_t *A,

@@ -219,6 +219,79 @@ def test_linear_schedules(M, N, K, r):
     check_layer(M, N, K, r, qlora.FP4_NVFP4 if r != 24 else qlora.FP4_MXFP4)
 
 
+def product(a, b):
+    """a b of small fp64 matrices term by term: a library's product may add 0 times an infinity."""
+    with np.errstate(invalid="ignore"):
+        return np.stack([(a[:, :, None] * b[None, :, j:j + 8]).sum(1) for j in range(0, b.shape[1], 8)], 1).reshape(
+            a.shape[0], b.shape[1])
+
+
+def same_class(got, want, what):
+    """Infinities with their signs and NaNs where the formula has them, finite values elsewhere."""
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want)), what
+    assert np.array_equal(np.isposinf(got), np.isposinf(want)) and np.array_equal(np.isneginf(got), np.isneginf(want)), what
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [5, 100, 300, 1100])
+def test_layer_with_values_that_are_not_finite(M, fmt):
+    """An infinity or a NaN in each operand in turn. G and T are exact in bf16 in half of the columns,
+    so that their lower parts are 0 there."""
+    N, K, r, scale, inf, nan = 96, 64, 8, 0.5, float("inf"), float("nan")
+    W, A, B, X, dY = (t.clone() for t in layer(51, M, N, K, r, fmt))
+    X[X == 0], dY[dY == 0] = 0.5, 0.25                     # no 0 times an infinity but where it is meant
+    q = qlora.qlora_fp4_quantize_weight(W.cuda(), fmt)
+    T = torch.from_numpy(np.random.default_rng(5).normal(0, 1, (M, r))).float()
+    T[:, ::2] = T[:, ::2].to(torch.bfloat16).float()
+
+    def run(X, T, dY, A, B):
+        Y, _ = qlora.qlora_fp4_linear_fwd(X.cuda(), q, A.cuda(), B.cuda(), scale)
+        dX, dA, dB = qlora.qlora_fp4_linear_bwd(dY.cuda(), X.cuda(), T.cuda(), q, A.cuda(), B.cuda(), scale)
+        X, T, dY, A, B = (t.double().numpy() for t in (X, T, dY, A, B))
+        with np.errstate(invalid="ignore", over="ignore"):
+            G = product(dY, B.T)
+            return Y, dX, dA, dB, product(product(X, A), B), product(G, A.T), product(X.T, G), product(T.T, dY)
+
+    def put(t, *at):
+        t = t.clone()
+        for i, j, v in at:
+            t[i, j] = v
+        return t
+    base = run(X, T, dY, A, B)
+    for got, what in zip(base[:4], ("Y", "dX", "dA", "dB")):
+        assert torch.isfinite(got).all(), what
+    m = M - 2
+    # T: dB alone
+    out = run(X, put(T, (m, 1, inf), (0, 2, -inf), (1, 3, nan)), dY, A, B)
+    assert torch.equal(out[0], base[0]) and torch.equal(out[1], base[1]) and torch.equal(out[2], base[2])
+    same_class(out[3], out[7], "dB of T")
+    # X: its rows of Y, its rows of dA
+    out = run(put(X, (m, 5, inf), (0, 9, -inf), (1, 40, nan)), T, dY, A, B)
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[[m, 0, 1]] = True
+    assert torch.isnan(out[0][bad]).all() and torch.equal(out[0][~bad], base[0][~bad])
+    assert torch.equal(out[1], base[1]) and torch.equal(out[3], base[3])
+    same_class(out[2], out[6], "dA of X")
+    # X against a G that is exact in bf16, so that its lower parts are 0
+    one = put(torch.zeros_like(dY), (m, 7, 1.0))
+    out = run(put(X, (m, 5, inf)), T, one, A, B)
+    same_class(out[2][5], out[6][5], "dA of X, exact G")
+    # dY: its rows of dX, columns of dB, and dA through G
+    out = run(X, T, put(dY, (m, 11, -inf)), A, B)
+    assert torch.isnan(out[1][m]).all()
+    keep = torch.arange(M, device="cuda") != m
+    assert torch.equal(out[1][keep], base[1][keep])
+    same_class(out[2], out[6], "dA of dY")
+    same_class(out[3], out[7], "dB of dY")
+    # A: Y through T; B: dA and dX through G
+    out = run(X, T, dY, put(A, (3, 2, inf)), B)
+    same_class(out[0], out[4], "Y of A")
+    out = run(X.abs(), T, dY.abs(), A, put(B, (4, 13, -inf)))
+    same_class(out[1], out[5], "dX of B")
+    same_class(out[2], out[6], "dA of B")
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_gradients_against_differences(fmt):
     """The layer without its roundings is linear in A and in B and, on the 4-bit grid, in X: the
