@@ -853,12 +853,13 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
               : u == 2 ? k_fp4_quantize_nv<BF16, 2>
               : u == 4 ? k_fp4_quantize_nv<BF16, BF16 ? 4 : 0>
                        : k_fp4_quantize_nv<BF16, 0>;
-  // A CTA a row; as many CTAs as run at one time, each taking several rows, where a row is short
-  // (they fetch the next one ahead; 4096 x 1024: 4.4 us against 4.8) and where the 64 registers
+  // A CTA a row; as many CTAs as run at one time (32 an SM at most: 8192 x 512 takes 5.4 us, 7.8
+  // with 48), each taking several rows, where a row is short (they fetch the next one ahead;
+  // 4096 x 1024: 4.4 us against 4.8) and where the 64 registers
   // of fp32 leave room for few CTAs, two from 352 threads on (8192 x 11008: 74 us against 79,
   // 4096 x 16384 48.5 against 53.0; 4096 x 8192, 256 threads: 28.0 against 24.8).
   const bool resident = u == 1 || (u > 0 && !BF16 && threads > 256);
-  const int64_t at_once = static_cast<int64_t>(num_sms()) * ((u == 1 ? 1536 : 1024) / threads);
+  const int64_t at_once = static_cast<int64_t>(num_sms()) * std::min(32, (u == 1 ? 1536 : 1024) / threads);
   const int64_t grid = resident ? std::min(rows, at_once) : rows;
   return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, st, X,
                     static_cast<uint32_t>(rows), cols, codes, scales, gscale);
