@@ -293,6 +293,91 @@ def test_layer_with_values_that_are_not_finite(M, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [5, 100, 300, 1100])
+def test_gradients_hold_T_and_G_to_the_last_bit(M, fmt):
+    """dB with one 1 in each column of dY is that token's T, and dA with one 1 in each column of X that
+    token's G, 24 bits of each: three bf16 parts hold 8 bits each, and adding them to one another and
+    to zeros is exact in fp32. G is a sum of three products of 8 bits at 1, 2^-8 and 2^-16, whose partial
+    sums are fp32 numbers."""
+    N, K, r = 160, 96, 16
+    g = np.random.default_rng(M)
+    W, A, X = normal(61, N, K, std=0.02), normal(62, K, r, std=0.02), normal(63, M, K)
+    q = qlora.qlora_fp4_quantize_weight(W.cuda(), fmt)
+    T = torch.from_numpy(g.uniform(1, 2, (M, r)) * g.choice([-1.0, 1.0], (M, r))).float()
+    assert (T.view(torch.int32) & 0xFF).any()                # bits of the third part
+    tok = g.integers(0, M, N)
+    dY = torch.zeros(M, N)
+    dY[tok, np.arange(N)] = 1.0
+    B = normal(64, r, N, std=0.02)
+    for need_dX in (True, False):
+        _, _, dB = qlora.qlora_fp4_linear_bwd(dY.to(torch.bfloat16).cuda(), X.cuda(), T.cuda(), q, A.cuda(), B.cuda(),
+                                              1.0, need_dX=need_dX)
+        assert torch.equal(dB.cpu(), T[tok].t())
+    # G[m, j] = B[j, n0] + B[j, n1] + B[j, n2], the columns in three different places of N
+    bits = g.integers(128, 256, (3, r, N)).astype(np.float64)
+    B = np.zeros((r, N))
+    for i, cols in enumerate((slice(0, 40), slice(40, 100), slice(100, N))):
+        B[:, cols] = bits[i][:, cols] * 2.0 ** (-7 - 8 * i)
+    n = np.stack([g.integers(0, 40, M), g.integers(40, 100, M), g.integers(100, N, M)])
+    dY = torch.zeros(M, N)
+    for i in range(3):
+        dY[np.arange(M), n[i]] = 1.0
+    G = dY.double().numpy() @ B.T
+    assert np.array_equal(G, G.astype(np.float32)) and (G.astype(np.float32).view(np.int32) & 0xFF).any()
+    tok = g.integers(0, M, K)
+    X = torch.zeros(M, K)
+    X[tok, np.arange(K)] = 1.0
+    for need_dX in (True, False):
+        _, dA, _ = qlora.qlora_fp4_linear_bwd(dY.to(torch.bfloat16).cuda(), X.to(torch.bfloat16).cuda(), T.cuda(), q, A.cuda(),
+                                              torch.from_numpy(B).to(torch.bfloat16).cuda(), 1.0, need_dX=need_dX)
+        assert np.array_equal(dA.double().cpu().numpy(), G[tok])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("gscale", [None, 0.37, 2.9e-4])
+@pytest.mark.parametrize("M", [3, 90, 200, 1100])
+def test_layer_on_any_gscale(M, gscale, fmt):
+    """A weight whose gscale is no power of two, one in MXFP4 that has a gscale, one in NVFP4 without:
+    the rank-r term is carried in its units."""
+    N, K, r, scale = 160, 288, 16, 0.5
+    W, A, B, X, dY = layer(71 + M, M, N, K, r, fmt)
+    q = qlora.qlora_fp4_quantize_weight(W.cuda(), fmt)
+    g = None if gscale is None else torch.tensor([gscale], device="cuda")
+    q.w.gscale = q.wt.gscale = g
+    w, _ = F.quantize_weight(W.double().numpy(), fmt)
+    w["g"] = np.ones(1) if g is None else g.double().cpu().numpy()
+    Y, T = qlora.qlora_fp4_linear_fwd(X.cuda(), q, A.cuda(), B.cuda(), scale)
+    dX, dA, dB = qlora.qlora_fp4_linear_bwd(dY.cuda(), X.cuda(), None, q, A.cuda(), B.cuda(), scale)
+    A64, B64, X64, dY64 = (t.double().numpy() for t in (A, B, X, dY))
+    Y64, T64 = F.linear_forward(X64, w, A64, B64, scale)
+    dX64, dA64, dB64 = F.linear_backward(dY64, X64, w, A64, B64, scale)
+    a = np.abs
+    Wv, Xq, dYq = F.dequant(w), F.dequant(F.quantize(X64, fmt)), F.dequant(F.quantize(dY64, fmt))
+    T_tol, G64 = (K / 16 + 80) * U * (a(X64) @ a(A64)), dY64 @ B64.T
+    G_tol = (N / 16 + 80) * U * (a(dY64) @ a(B64).T)
+    lora = lambda v, tol, m: abs(scale) * ((PAIR + 16 * U) * (a(v) @ a(m)) + tol @ a(m))
+    within(T, T64, T_tol, "T")
+    tol = product_tol(Xq, Wv) + lora(T64, T_tol, B64)
+    within(Y, Y64, tol + BF16 * (a(Y64) + tol), "Y")
+    tol = product_tol(dYq, Wv.T) + lora(G64, G_tol, A64.T)
+    within(dX, dX64, tol + BF16 * (a(dX64) + tol), "dX")
+    steps = (M / 16 + 80) * U
+    within(dA, dA64, abs(scale) * (steps * (a(X64).T @ a(G64)) + a(X64).T @ G_tol), "dA")
+    within(dB, dB64, abs(scale) * (steps * (a(T64).T @ a(dY64)) + T_tol.T @ a(dY64)), "dB")
+
+
+@pytest.mark.parametrize("M,N,K,r", [(2, 96, 8256, 8), (100, 8256, 96, 64), (2600, 288, 4128, 64),
+                                     (300, 12544, 160, 40), (17, 20000, 64, 16), (1300, 4128, 160, 16)])
+def test_linear_schedules_in_mxfp4(M, N, K, r):
+    check_layer(M, N, K, r, qlora.FP4_MXFP4)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_linear_recomputes_T_of_a_large_batch(fmt):
+    check_layer(1100, 160, 320, 16, fmt, saved_T=False)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_gradients_against_differences(fmt):
     """The layer without its roundings is linear in A and in B and, on the 4-bit grid, in X: the
     difference of two outputs along a direction is the gradient's inner product with it. The
