@@ -1,7 +1,8 @@
 """Build the C-ABI library ``lib/libqlora.so`` from ``csrc/`` with nvcc for sm_100a.
 
 The Python calls of the microscaled 4-bit operators go through a second, small library,
-``lib/qlora_binding.so`` (g++, torch's headers), which loads the first.
+``lib/qlora_binding.so`` (g++, torch's headers), which loads the first. Where torch or the headers
+are not installed the C library is built alone (``python bit_nf4_quantized_unpack_b200/build.py``).
 
 Run ``python -m bit_nf4_quantized_unpack_b200.build`` (or call ``build()``). Objects go
 to ``_build/`` at the repository root; the library is written in-tree next to this
@@ -10,10 +11,12 @@ file so that it ships with a snapshot of the repository.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -60,13 +63,28 @@ def _compile(src, verbose):
     return obj, res.stderr if verbose else ""
 
 
-def build_binding(force: bool = False) -> str:
-    """Compile the Python binding against the running interpreter's torch."""
+def _binding_lacks():
+    """What the Python binding cannot be compiled without and is not installed here, or None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return "torch"
+    for path in (os.path.join(os.path.dirname(spec.origin), "include", "torch", "csrc", "utils", "pybind.h"),
+                 os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(path):
+            return path
+    return None
+
+
+def build_binding(force: bool = False) -> str | None:
+    """Compile the Python binding against the running interpreter's torch. Returns its path, or None
+    where torch or a header is missing (its calls then raise)."""
+    lacks = _binding_lacks()
+    if lacks:
+        sys.stderr.write(f"{os.path.basename(BINDING)} is left out: no {lacks}\n")
+        return None
     newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "qlora.h"), __file__))
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
         return BINDING
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
@@ -89,7 +107,8 @@ def build_binding(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA/C++ source for sm_100a and link the shared library, and the Python
-    binding. Returns the library path. Skips what is newer than its sources."""
+    binding where torch and its headers are installed. Returns the library path. Skips what is
+    newer than its sources."""
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
         binding = ex.submit(build_binding, force)
         path = _build_library(force, verbose)
