@@ -63,6 +63,13 @@ def _compile(src, verbose):
     return obj, res.stderr if verbose else ""
 
 
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _binding_lacks():
     """What the Python binding cannot be compiled without and is not installed here, or None."""
     spec = importlib.util.find_spec("torch")
@@ -82,18 +89,22 @@ def build_binding(force: bool = False) -> str | None:
     if lacks:
         sys.stderr.write(f"{os.path.basename(BINDING)} is left out: no {lacks}\n")
         return None
-    newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "qlora.h"), __file__))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
     import torch
+    newest = max(os.path.getmtime(p) for p in (BINDING_SRC, os.path.join(INCLUDE, "qlora.h"), __file__))
+    stamp = os.path.join(OBJ, "qlora_binding.torch")  # what the binding was compiled for
+    built_for = f"{sys.implementation.cache_tag} torch {torch.__version__}"
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and _read(stamp) == built_for:
+        return BINDING
     root = os.path.dirname(torch.__file__)
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     includes = [os.path.join(root, "include"),
                 os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 cuda_inc, sysconfig.get_paths()["include"]]
     os.makedirs(os.path.dirname(BINDING), exist_ok=True)
+    os.makedirs(OBJ, exist_ok=True)
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden",
+           f'-DQLORA_TORCH_VERSION="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[a for i in includes for a in ("-isystem", i)], BINDING_SRC, "-o", tmp,
            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
@@ -102,6 +113,8 @@ def build_binding(force: bool = False) -> str | None:
     if res.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return BINDING
 
 

@@ -343,6 +343,7 @@ py::tuple linear_bwd(const Tensor& dY, const Tensor& X, const OptTensor& T, cons
 }  // namespace
 
 PYBIND11_MODULE(qlora_binding, m) {
+  m.attr("torch_version") = QLORA_TORCH_VERSION;  // tensors of another torch may be laid out otherwise
   m.def("open", &open);
   m.def("quantize", &quantize);
   m.def("quantize_out", &quantize_out);

@@ -491,6 +491,9 @@ def binding():
         spec = importlib.util.spec_from_file_location("qlora_binding", BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        if module.torch_version != torch.__version__:
+            raise RuntimeError(f"{BINDING_PATH} was built for torch {module.torch_version}, this is {torch.__version__}: "
+                               "build it again with `python -m bit_nf4_quantized_unpack_b200.build`")
         module.open(LIB_PATH, QLoraError)
         _binding = module
     return _binding
