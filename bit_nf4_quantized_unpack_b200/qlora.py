@@ -562,14 +562,18 @@ def qlora_fp4_quantize_weight(W: torch.Tensor, fmt: int = FP4_NVFP4, transposed:
                               out: FP4Weight | None = None,
                               workspace: torch.Tensor | None = None) -> FP4Weight:
     """W [n_out, k_in] (fp32 or bf16, CUDA, contiguous, multiples of 32) with square blocks;
-    transposed: also the copy that the backward reads (w and wt share one gscale)."""
+    transposed: also the copy that the backward reads (w and wt share one gscale). out: both of its
+    matrices are written, or w alone where it has no wt; an out with a wt and transposed=False is
+    refused, as its wt would go on holding another weight's values under this one's gscale."""
     ext = _binding or binding()
     if out is None:
         c, s, g, tc, ts = ext.weight(W, fmt, transposed, workspace)
         n, k = W.shape
         return FP4Weight(FP4Matrix(c, s, g, n, k, fmt),
                          FP4Matrix(tc, ts, g, k, n, fmt) if transposed else None)
-    w, wt = out.w, out.wt if transposed else None
+    w, wt = out.w, out.wt
+    if wt is not None and not transposed:
+        raise ValueError("out.wt: not written with transposed=False, pass FP4Weight(out.w)")
     n, k = W.shape
     if (w.rows, w.cols, w.fmt) != (n, k, fmt) or (
             wt is not None and (wt.rows, wt.cols, wt.fmt) != (k, n, fmt)):

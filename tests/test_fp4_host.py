@@ -129,3 +129,13 @@ def test_mxfp4_output_with_a_gscale_is_refused():
     with pytest.raises(ValueError, match="gscale"):
         qlora.qlora_fp4_quantize_weight(torch.zeros(64, 64), qlora.FP4_MXFP4, transposed=False,
                                         out=qlora.FP4Weight(q))
+
+
+@pytest.mark.parametrize("fmt", [qlora.FP4_MXFP4, qlora.FP4_NVFP4])
+def test_weight_output_whose_transpose_would_go_stale_is_refused(fmt):
+    """transposed=False into a weight that has a transposed copy would leave the copy's old codes, which
+    the backward would multiply by under the new gscale."""
+    out = qlora.FP4Weight(qlora.FP4Matrix.empty(64, 96, fmt, device="cpu", gscale_rows=1),
+                          qlora.FP4Matrix.empty(96, 64, fmt, device="cpu", gscale_rows=1))
+    with pytest.raises(ValueError, match="out.wt"):
+        qlora.qlora_fp4_quantize_weight(torch.zeros(64, 96), fmt, transposed=False, out=out)
