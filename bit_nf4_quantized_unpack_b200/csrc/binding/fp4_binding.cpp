@@ -180,7 +180,8 @@ py::tuple quantize(const Tensor& X, int fmt) {
   const int64_t rows = X.size(0), cols = X.size(1);
   const void* x = dense(X, "X", dev, X.scalar_type(), X.sizes());
   const size_t nsc = L.scales_bytes(rows, cols, fmt);
-  if (nsc == 0 && rows != 0) check(QLORA_ERR_SHAPE, "qlora_fp4_quantize");
+  if (nsc == 0 && rows != 0)  // no such format or shape: the entry point says which
+    check(L.quantize(x, dt, rows, cols, fmt, nullptr, nullptr, nullptr, nullptr), "qlora_fp4_quantize");
   const int64_t sc = static_cast<int64_t>(nsc);
   Bytes b(Bytes::room(rows * (cols / 2)) + sc, dev);
   const Tensor codes = b.take({rows, cols / 2}), scales = b.take({sc});
@@ -232,12 +233,15 @@ void weight_out(const Tensor& W, int fmt, const Tensor& codes, const Tensor& sca
 
 // (codes, scales, gscale or None, t_codes or None, t_scales or None) of W [n, k]
 py::tuple weight(const Tensor& W, int fmt, bool transposed, const OptTensor& workspace) {
-  dtype_of(W, "W");
+  const qlora_dtype dt = dtype_of(W, "W");
   const auto dev = device_of(W, "W");
   check_2d(W, "W");
   const int64_t n = W.size(0), k = W.size(1);
   const size_t nsc = L.scales_bytes(n, k, fmt), tsc = L.scales_bytes(k, n, fmt);
-  if (nsc == 0 || (transposed && tsc == 0)) check(QLORA_ERR_SHAPE, "qlora_fp4_quantize_weight");
+  if (nsc == 0 || (transposed && tsc == 0)) {  // no such format or shape: the entry point says which
+    check(L.quantize_weight(nullptr, dt, n, k, fmt, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, nullptr),
+          "qlora_fp4_quantize_weight");
+  }
   const int64_t sc = static_cast<int64_t>(nsc), st = static_cast<int64_t>(tsc);
   const int64_t wsb = workspace ? 0 : static_cast<int64_t>(L.weight_workspace());
   Bytes b(Bytes::room(n * (k / 2)) + Bytes::room(sc) + wsb, dev);

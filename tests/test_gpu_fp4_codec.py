@@ -240,3 +240,19 @@ def test_tiny_and_huge_rows(fmt):
         W = x[row].repeat(32, 1)[:, :32].contiguous()
         w = qlora.qlora_fp4_quantize_weight(W.cuda(), fmt)
         same_matrix(w.w, F.quantize_weight(W.double().numpy(), fmt)[0], row)
+
+
+def test_refusals_name_their_reason():
+    """An unknown format is an invalid argument (1), columns or rows that are no multiple a shape (2)."""
+    def status(fn, *args, **kw):
+        with pytest.raises(qlora.QLoraError) as e:
+            fn(*args, **kw)
+        return e.value.status
+    x, odd = torch.zeros(64, 64, device="cuda"), torch.zeros(64, 48, device="cuda")
+    for fn in (qlora.qlora_fp4_quantize, qlora.qlora_fp4_quantize_weight):
+        assert status(fn, x, 7) == 1 and status(fn, x, -1) == 1
+        assert status(fn, odd) == 2 and status(fn, odd[:, :0].contiguous()) == 2
+    assert status(qlora.qlora_fp4_quantize, x[:0], 7) == 1
+    assert status(qlora.qlora_fp4_quantize_weight, x[:40]) == 2
+    assert status(qlora.qlora_fp4_quantize_weight, x[:40], transposed=False) == 2
+    assert status(qlora.qlora_fp4_quantize_weight, x[:0]) == 2
