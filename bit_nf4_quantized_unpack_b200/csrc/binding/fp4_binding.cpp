@@ -223,8 +223,8 @@ void weight_out(const Tensor& W, int fmt, const Tensor& codes, const Tensor& sca
     throw py::value_error("out.w.gscale: expected one value");
   qlora_fp4_matrix t = {};
   if (t_codes && t_scales) t = matrix(*t_codes, *t_scales, std::nullopt, k, n, fmt, "out.wt", dev);
-  const Workspace ws(workspace, L.weight_workspace(), dev);
   const Launch l(dev);
+  const Workspace ws(workspace, L.weight_workspace(), dev);
   check(L.quantize_weight(src, dt, n, k, fmt, const_cast<uint8_t*>(m.codes), const_cast<uint8_t*>(m.scales),
                           const_cast<float*>(m.gscale), const_cast<uint8_t*>(t.codes),
                           const_cast<uint8_t*>(t.scales), ws.ptr, ws.bytes, l.stream),
@@ -307,8 +307,8 @@ py::tuple linear_fwd(const Tensor& X, const Tensor& wc, const Tensor& ws_, const
     t = static_cast<float*>(dense(T, "T", dev, at::kFloat, {M, r}));
   }
   const int ri = static_cast<int>(r > 1 << 20 ? 1 << 20 : r);
+  const Launch l(dev);  // before the query: the rank-r products' splits go by the device's SMs
   const Workspace ws(workspace, L.fwd_workspace(M, n, k, ri, fmt), dev);
-  const Launch l(dev);
   check(L.fwd(x, M, w, a, b, ri, static_cast<float>(scale), y, t, ws.ptr, ws.bytes, l.stream),
         "qlora_fp4_linear_fwd");
   return py::make_tuple(Y, save_T ? py::cast(T) : py::none());
@@ -337,8 +337,8 @@ py::tuple linear_bwd(const Tensor& dY, const Tensor& X, const OptTensor& T, cons
   auto* da = static_cast<float*>(dense(dA, "dA", dev, at::kFloat, {k, r}));
   auto* db = static_cast<float*>(dense(dB, "dB", dev, at::kFloat, {r, n}));
   const int ri = static_cast<int>(r > 1 << 20 ? 1 << 20 : r);
-  const Workspace ws(workspace, L.bwd_workspace(M, n, k, ri, fmt), dev);
   const Launch l(dev);
+  const Workspace ws(workspace, L.bwd_workspace(M, n, k, ri, fmt), dev);
   check(L.bwd(dy, x, t, M, wt, a, b, ri, static_cast<float>(scale), dx, da, db, ws.ptr, ws.bytes, l.stream),
         "qlora_fp4_linear_bwd");
   return py::make_tuple(need_dX ? py::cast(dX) : py::none(), dA, dB);
