@@ -35,6 +35,12 @@ qlora_status check_matrix(const qlora_fp4_matrix& q) {
   return QLORA_OK;
 }
 
+// Whether `an` bytes at a and `bn` bytes at b share memory.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
 bool finite_scale(float s) { return s == s && s <= 3.0e38f && s >= -3.0e38f; }
 
 // The checks both directions of the linear layer share; w is the weight in either form.
@@ -197,6 +203,10 @@ qlora_status qlora_fp4_linear_bwd(const uint16_t* dY, const uint16_t* X, const f
     return QLORA_ERR_ALIGN;
   if (!workspace || workspace_bytes < fp4_bwd_workspace(s, wt.format)) return QLORA_ERR_WORKSPACE;
   if (!is_aligned16(workspace)) return QLORA_ERR_ALIGN;
+  // dA and dB read X and dY beside or behind the product that writes dX
+  const size_t x_bytes = static_cast<size_t>(M) * s.K * 2, y_bytes = static_cast<size_t>(M) * s.N * 2;
+  if (dX && (overlap(dX, x_bytes, X, x_bytes) || overlap(dX, x_bytes, dY, y_bytes)))
+    return QLORA_ERR_INVALID_ARG;
   q = check_device();
   if (q != QLORA_OK) return q;
   return fp4_backward(dY, X, T_saved, wt, A, B, s, dX, dA, dB, workspace, st);

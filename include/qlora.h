@@ -512,7 +512,8 @@ size_t qlora_fp4_linear_bwd_workspace_size(int64_t M, int64_t n_out, int64_t k_i
  * for the large product only; G, dA and dB see the 16-bit dY. Infinities reach dA and dB as the
  * formulas say (a G or T beyond bf16's largest number counts as one). A NaN or an infinity in
  * a row of dY makes that row of dX NaN and no other; one in A comes out in dX as an infinity or a
- * NaN. Other arguments, layouts and errors as qlora_linear_bwd.
+ * NaN. Other arguments, layouts and errors as qlora_linear_bwd; QLORA_ERR_INVALID_ARG too for
+ * a dX that shares memory with X or dY, which dA and dB still read while it is written.
  */
 qlora_status qlora_fp4_linear_bwd(const uint16_t *dY, const uint16_t *X, const float *T_saved,
                                   int64_t M, qlora_fp4_matrix wt, const uint16_t *A,

@@ -139,3 +139,15 @@ def test_weight_output_whose_transpose_would_go_stale_is_refused(fmt):
                           qlora.FP4Matrix.empty(96, 64, fmt, device="cpu", gscale_rows=1))
     with pytest.raises(ValueError, match="out.wt"):
         qlora.qlora_fp4_quantize_weight(torch.zeros(64, 96), fmt, transposed=False, out=out)
+
+
+def test_backward_in_place_is_refused(L):
+    """dX over X or dY, which dA and dB read beside or behind the product that writes it: the same
+    address, and ranges that overlap at either end (64 x 1024 and 64 x 512 bf16)."""
+    need = L.qlora_fp4_linear_bwd_workspace_size(64, 512, 1024, 8, 1)
+    x, dy = 1 << 24, 1 << 26
+
+    def bwd(dX):
+        return L.qlora_fp4_linear_bwd(dy, x, None, 64, mat(1024, 512), P, P, 8, 1.0, dX, P, P, P, need, None)
+    for dX in (x, dy, x + 131072 - 16, x - 131072 + 16, dy + 65536 - 16, dy - 131072 + 16):
+        assert bwd(dX) == 1, dX

@@ -469,6 +469,21 @@ def test_caller_buffers_and_refusals_on_the_device():
         qlora.qlora_fp4_matmul(mx, q.w)
 
 
+@pytest.mark.parametrize("M", [20, 200])
+def test_backward_into_its_inputs_is_refused_and_beside_them_is_not(M):
+    W, A, B, X, dY = (t.cuda() for t in layer(43, M, 96, 96, 8, 1))
+    q = qlora.qlora_fp4_quantize_weight(W)
+    for dX in (X, dY):
+        with pytest.raises(qlora.QLoraError) as e:
+            qlora.qlora_fp4_linear_bwd(dY, X, None, q, A, B, 1.0, dX=dX)
+        assert e.value.status == 1
+    want = qlora.qlora_fp4_linear_bwd(dY, X, None, q, A, B, 1.0)
+    both = torch.cat([X, torch.zeros_like(X), dY])           # dX between X and dY, all touching
+    got = qlora.qlora_fp4_linear_bwd(both[2 * M:], both[:M], None, q, A, B, 1.0, dX=both[M:2 * M])
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(both[:M], X) and torch.equal(both[2 * M:], dY)
+
+
 def test_streams_and_graphs():
     """The same bits on another stream, in a captured and replayed graph with new inputs, and
     from two streams at once."""
