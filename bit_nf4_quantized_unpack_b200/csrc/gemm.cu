@@ -1314,19 +1314,38 @@ qlora_status gemm_shard_bwd(const uint16_t* dY, const uint16_t* X, const float* 
 // ---- the linear layer on a microscaled 4-bit weight: the same rank-r products, with the
 // 16-bit X and dY; only the large product sees their 4-bit form.
 namespace {
-// Quantizing (unless `quantize` is false) beside the rank-r product that reads the same rows; NVFP4,
-// N = K = 4096, r = 64. From kSideM tokens the quantizer fills the SMs: the product runs first,
-// the quantizer on the side stream (4096 tokens, in a graph: forward 49.9 us, in order 53.4;
-// backward 73.6, 76.8). Below, events between streams cost an eager call more than the
-// overlap gives (512 tokens, backward: 35.1 us, in order 33.0). There the product is told
-// (`true`) that it may start behind the quantizer without waiting for it (512 tokens,
-// forward: 20.7 us, waiting 22.8).
-constexpr int64_t kSideM = 1024;
+// Quantizing (unless `quantize` is false) beside the rank-r product that reads the same rows, on the
+// side stream while the product runs on the caller's; or in order, where the product is told (`true`) that it
+// may start behind the quantizer without waiting for it (512 x 4096 x 4096, forward: 20.7 us,
+// waiting 22.8). Events between streams cost an eager call 2-3 us and a graph nothing. NVFP4, r = 64,
+// side stream (in order), us:
+//   tokens x N x K           eager forward  eager backward  graph forward   graph backward
+//    512 x  4096 x  4096      25.1 (22.5)    38.1 (35.7)     20.9 (20.7)     31.7 (32.4)
+//   1024 x  4096 x  4096      26.5 (24.9)    42.2 (39.4)     22.3 (23.3)     34.2 (35.6)
+//   1024 x  4096 x 11008      41.2 (38.6)    58.8 (55.9)     36.3 (36.9)     50.4 (51.8)
+//   2048 x  4096 x  4096      34.6 (32.8)    54.9 (52.4)     30.9 (31.2)     46.3 (47.4)
+//   2048 x 11008 x  4096      57.5 (55.1)    90.4 (85.9)     53.9 (54.0)     81.7 (85.3)
+//   4096 x  4096 x  4096      55.2 (52.7)    82.4 (80.8)     49.6 (50.9)     74.0 (76.5)
+//   4096 x  4096 x 11008     114.1 (115.3)  140.3 (141.7)   118.6 (129.7)   154.2 (159.7)
+//   4096 x 11008 x  4096     101.5 (99.7)   158.9 (164.6)   108.1 (111.2)   159.3 (169.9)
+// So: the side stream from 512 tokens in a capture (256 tokens differ either way, by up to 12 %), from 4096 in
+// an eager call.
+constexpr int64_t kSideM = 4096, kSideCaptureM = 512;
+cudaError_t quantizer_stream(cudaStream_t st, int64_t M, SideStream** side) {
+  *side = nullptr;
+  if (M < kSideCaptureM) return cudaSuccess;
+  cudaError_t e = side_stream(st, side);  // made by an eager call, used or not: a capture cannot make it
+  if (e != cudaSuccess || M >= kSideM) return e;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  e = cudaStreamIsCapturing(st, &cs);
+  if (cs == cudaStreamCaptureStatusNone) *side = nullptr;
+  return e;
+}
 template <typename Quantizer, typename Product>
 cudaError_t quantize_and_rank(cudaStream_t st, int64_t M, bool quantize, Quantizer&& quantizer, Product&& product) {
   if (!quantize) return product(st, false);
   SideStream* side = nullptr;
-  cudaError_t e = M >= kSideM ? side_stream(st, &side) : cudaSuccess;
+  cudaError_t e = quantizer_stream(st, M, &side);
   if (e != cudaSuccess) return e;
   if (!side) {
     e = quantizer(st);

@@ -563,6 +563,40 @@ def test_large_batch_on_streams_and_in_graphs(fmt):
             assert all(torch.equal(x, y) for x, y in zip(out, ref))
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [600, 4200])
+def test_quantizer_on_and_off_the_side_stream(M, fmt):
+    """Beside the rank-r product (in a capture, and in an eager call of many tokens) or in order: the formulas,
+    and the same bits in eager calls, on two streams at once and in a replayed graph."""
+    check_layer(M, 96, 160, 16, fmt)
+    W, A, B, X, dY = (t.cuda() for t in layer(19, M, 96, 160, 16, fmt))
+    q = qlora.qlora_fp4_quantize_weight(W, fmt)
+
+    def step(x, dy):
+        y, t = qlora.qlora_fp4_linear_fwd(x, q, A, B, 0.5)
+        return (y, t) + qlora.qlora_fp4_linear_bwd(dy, x, t, q, A, B, 0.5)
+    ins = [(X, dY), (X.flip(0).contiguous(), dY.flip(0).contiguous())]
+    want = [step(*i) for i in ins]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [None, None]
+    for _ in range(3):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i] = step(*ins[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(got[i], want[i]))
+    bx, bdy = X.clone(), dY.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(bx, bdy)
+    for i in (1, 0, 1):
+        bx.copy_(ins[i][0]), bdy.copy_(ins[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want[i]))
+
+
 @pytest.mark.parametrize("M", [2, 150, 700, 1100])
 def test_calls_back_to_back_on_one_buffer(M):
     """Kernels of a call start before their predecessors end: the input rewritten between calls
