@@ -373,6 +373,75 @@ def test_linear_schedules_in_mxfp4(M, N, K, r):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,r,scale", [
+    (130, 32, 32, 8, 0.5), (1000, 64, 32, 64, 0.5), (200, 96, 416, 56, -2.0), (70, 96, 160, 48, -2.0),
+    (3, 64, 64, 8, 0.0), (200, 64, 64, 8, 0.0)])
+def test_linear_smallest_weights_ranks_and_scales(M, N, K, r, scale, fmt):
+    check_layer(M, N, K, r, fmt, scale=scale)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_codec_and_product_in_a_graph(fmt):
+    """A weight laid out, activations quantized, their product and both read back, captured once and
+    replayed on new inputs, and the same calls on a stream of their own."""
+    M, N, K = 300, 160, 288
+    def step(x, w):
+        q, a = qlora.qlora_fp4_quantize_weight(w, fmt), qlora.qlora_fp4_quantize(x, fmt)
+        return (qlora.qlora_fp4_matmul(a, q.w), qlora.qlora_fp4_matmul(a, q.w, torch.float32),
+                qlora.qlora_fp4_dequant(a), qlora.qlora_fp4_dequant(q.w), qlora.qlora_fp4_dequant(q.wt, torch.float32))
+    ins = [(normal(s, M, K).cuda(), normal(s + 1, N, K, std=0.02).cuda()) for s in (81, 83)]
+    want = [step(*i) for i in ins]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = step(*ins[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want[0]))
+    x, w = (t.clone() for t in ins[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, w)
+    for i in (1, 0):
+        x.copy_(ins[i][0]), w.copy_(ins[i][1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_weight_offsets_past_32_bits(fmt):
+    """A weight of more than 2^32 values: its last rows and columns, in both orientations and as the
+    operand of a product."""
+    N, K = 65600, 65568
+    W = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    band, cols = normal(85, 64, K, std=0.02).cuda(), normal(86, N, 32, std=0.02).cuda()
+    W[:32], W[-64:] = band[:32], band
+    W[:, -32:] = cols
+    W[0, 0] = 1.0                                            # the matrix's largest value, in every part below
+    q = qlora.qlora_fp4_quantize_weight(W, fmt)
+    part = W[-64:].clone()
+    part[0, 0] = 1.0
+    p = qlora.qlora_fp4_quantize_weight(part, fmt)
+    assert torch.equal(q.w.codes[-32:], p.w.codes[-32:])
+    right = W[:, -64:].clone()
+    right[0, 0] = 1.0
+    t = qlora.qlora_fp4_quantize_weight(right, fmt)
+    assert torch.equal(q.wt.codes[-32:], t.wt.codes[-32:])
+    if fmt == qlora.FP4_NVFP4:
+        assert q.w.gscale.item() == p.w.gscale.item() == t.w.gscale.item()
+    for M in (3, 200):
+        x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+        x[:, -32:] = normal(87, M, 32).cuda()
+        a = qlora.qlora_fp4_quantize(x, fmt)
+        got = qlora.qlora_fp4_matmul(a, q.w, torch.float32)
+        small = qlora.qlora_fp4_quantize(x[:, -64:].contiguous(), fmt)
+        va, vb = (qlora.qlora_fp4_dequant(m, torch.float32).double() for m in (small, t.w))
+        va[:, :32] = 0
+        # all but 32 products are exact zeros: one group of 64 columns adds up, as in the small product
+        want, mag = (va @ vb.t()), va.abs() @ vb.abs().t()
+        assert ((got.double() - want).abs() <= 16 * U * mag).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_linear_recomputes_T_of_a_large_batch(fmt):
     check_layer(1100, 160, 320, 16, fmt, saved_T=False)
 
