@@ -106,7 +106,7 @@ __device__ __forceinline__ uint32_t finite_amax(const R& r) {
 }
 
 // x / d for positive normal d, correctly rounded: the reciprocal's product and one correction
-// by its exact remainder. (Results below the normal range only round to the code 0.)
+// by its exact remainder (Markstein's method, IBM J. Res. Dev. 34, 1990). (Results below the normal range only round to the code 0.)
 __device__ __forceinline__ float div_rn(float x, float d, float rcp) {
   const float q = x * rcp;
   return __fmaf_rn(__fmaf_rn(-q, d, x), rcp, q);

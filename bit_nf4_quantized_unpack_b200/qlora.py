@@ -588,14 +588,16 @@ def qlora_fp4_quantize_weight(W: torch.Tensor, fmt: int = FP4_NVFP4, transposed:
 
 def qlora_fp4_dequant(q: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
                       out: torch.Tensor | None = None) -> torch.Tensor:
-    """The values of a microscaled matrix [rows, cols], bf16 or fp32."""
+    """The values of a microscaled matrix [rows, cols], bf16 or fp32. out: written in its own type,
+    whatever dtype says."""
     return (_binding or binding()).dequant(q.codes, q.scales, q.gscale, q.rows, q.cols, q.fmt,
                                            _bf16(dtype), out)
 
 
 def qlora_fp4_matmul(a: FP4Matrix, b: FP4Matrix, dtype: torch.dtype = torch.bfloat16,
                      out: torch.Tensor | None = None) -> torch.Tensor:
-    """a b^T [a.rows, b.rows], bf16 or fp32; both operands of one format, b.rows % 8 == 0."""
+    """a b^T [a.rows, b.rows], bf16 or fp32; both operands of one format, b.rows % 8 == 0. out:
+    written in its own type, whatever dtype says."""
     return (_binding or binding()).matmul(a.codes, a.scales, a.gscale, a.rows, a.cols, a.fmt,
                                           b.codes, b.scales, b.gscale, b.rows, b.cols, b.fmt,
                                           _bf16(dtype), out)

@@ -434,7 +434,7 @@ size_t qlora_fp4_scales_bytes(int64_t rows, int64_t cols, int32_t format);
  * A NaN or an infinity makes its block's scale NaN and that block's codes 0, and does not
  * enter rowmax.
  *   codes, scales as above; gscale fp32 [rows] (NV; not used and may be NULL for MX)
- * rows == 0 enqueues nothing. Errors: QLORA_ERR_SHAPE unless 0 <= rows < 2^31 - 256,
+ * rows == 0 enqueues nothing. Errors: QLORA_ERR_SHAPE unless 0 <= rows <= 2^31 - 256,
  * 32 <= cols <= 2^28, cols % 32 == 0 and rows * cols <= 2^40; QLORA_ERR_INVALID_ARG for a NULL
  * pointer, an unknown dtype or format; QLORA_ERR_ALIGN unless the pointers are 16-byte aligned.
  */
