@@ -691,6 +691,57 @@ def test_calls_back_to_back_on_one_buffer(M):
         assert all(torch.equal(x, y) for x, y in zip(g, want[i % 3])), i
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [7, 128, 136, 600, 4200])
+def test_one_tensor_in_two_places(M, fmt):
+    """A matrix times its own transpose, one tensor as X and as dY, and a forward over its own input."""
+    N = K = 160
+    W, A, B, X, _ = (t.cuda() for t in layer(91, M, N, K, 16, fmt))
+    q, a = qlora.qlora_fp4_quantize_weight(W, fmt), qlora.qlora_fp4_quantize(X, fmt)
+    if M % 8 == 0:
+        copy = qlora.FP4Matrix(a.codes.clone(), a.scales.clone(), a.gscale, M, K, fmt)
+        p = qlora.qlora_fp4_matmul(a, a, torch.float32)
+        assert torch.equal(p, qlora.qlora_fp4_matmul(a, copy, torch.float32))
+    Y, T = qlora.qlora_fp4_linear_fwd(X, q, A, B, 0.5)
+    want = qlora.qlora_fp4_linear_bwd(X.clone(), X, T, q, A, B, 0.5)
+    got = qlora.qlora_fp4_linear_bwd(X, X, T, q, A, B, 0.5)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    over = X.clone()
+    Y1, T1 = qlora.qlora_fp4_linear_fwd(over, q, A, B, 0.5, Y=over)
+    assert torch.equal(over, Y) and torch.equal(T1, T)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_two_host_threads(fmt):
+    """Calls of two threads, each on its own stream, on one weight."""
+    import threading
+    W, A, B, X, dY = (t.cuda() for t in layer(93, 4200, 96, 160, 16, fmt))
+    q = qlora.qlora_fp4_quantize_weight(W, fmt)
+    sizes, bad, done = (5, 100, 300, 1100, 4200), [], []
+
+    def step(M):
+        y, t = qlora.qlora_fp4_linear_fwd(X[:M], q, A, B, 0.5)
+        return (y, t) + qlora.qlora_fp4_linear_bwd(dY[:M], X[:M], t, q, A, B, 0.5)
+    want = {M: step(M) for M in sizes}
+    torch.cuda.synchronize()
+
+    def work(order):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for i in range(20):
+                for M in order:
+                    got = step(M)
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(x, y) for x, y in zip(got, want[M])):
+                        bad.append((i, M))
+        done.append(order)
+    threads = [threading.Thread(target=work, args=(o,)) for o in (sizes, sizes[::-1])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(done) == 2 and not bad
+
+
 def test_training_step_on_a_microscaled_weight():
     """The operators together: lay the weight out, forward, backward, optimizer step, and the
     next forward on the updated adapter."""
