@@ -106,7 +106,8 @@ __device__ __forceinline__ uint32_t finite_amax(const R& r) {
 }
 
 // x / d for positive normal d, correctly rounded: the reciprocal's product and one correction
-// by its exact remainder (Markstein's method, IBM J. Res. Dev. 34, 1990). (Results below the normal range only round to the code 0.)
+// by its exact remainder (Markstein's method, IBM J. Res. Dev. 34, 1990). (Results below the
+// normal range only round to the code 0.)
 __device__ __forceinline__ float div_rn(float x, float d, float rcp) {
   const float q = x * rcp;
   return __fmaf_rn(__fmaf_rn(-q, d, x), rcp, q);
@@ -855,9 +856,9 @@ cudaError_t quantize_rows(const void* X, int64_t rows, int64_t cols, int format,
                        : k_fp4_quantize_nv<BF16, 0>;
   // A CTA a row; as many CTAs as run at one time (32 an SM at most: 8192 x 512 takes 5.4 us, 7.8
   // with 48), each taking several rows, where a row is short (they fetch the next one ahead;
-  // 4096 x 1024: 4.4 us against 4.8) and where the 64 registers
-  // of fp32 leave room for few CTAs, two from 352 threads on (8192 x 11008: 74 us against 79,
-  // 4096 x 16384 48.5 against 53.0; 4096 x 8192, 256 threads: 28.0 against 24.8).
+  // 4096 x 1024: 4.4 us against 4.8) and where the 64 registers of fp32 leave room for few CTAs, two
+  // from 352 threads on (8192 x 11008: 74 us against 79, 4096 x 16384 48.5 against 53.0;
+  // 4096 x 8192, 256 threads: 28.0 against 24.8).
   const bool resident = u == 1 || (u > 0 && !BF16 && threads > 256);
   const int64_t at_once = static_cast<int64_t>(num_sms()) * std::min(32, (u == 1 ? 1536 : 1024) / threads);
   const int64_t grid = resident ? std::min(rows, at_once) : rows;
